@@ -30,7 +30,9 @@
  *     out) write the first such bsa_status code there and never trap. A call whose
  *     inputs were found malformed leaves its outputs unwritten.
  *   - Supported: d in {64, 128}; block in {64, 128}; L % block == 0; M <= 2048.
- *     Anything else returns BSA_ERR_UNSUPPORTED.
+ *     Anything else returns BSA_ERR_UNSUPPORTED. (The calls around the block attention,
+ *     bsa_rotary, bsa_cross_forward and bsa_linear, take other shapes, types and
+ *     strided tensors: each says which.)
  *   - Token padding ([BSA] §4.1 pads the text segment to a multiple of the block size;
  *     §7.3 gives a timestep token its own block): `key_valid` (nullable, device int32
  *     [M], shared by every (batch, head)) is the number of leading real tokens of each
@@ -275,6 +277,60 @@ BSA_API bsa_status bsa_selftest_forward_timeout(const void* Q, const void* K, co
                                                 const float* vsum, const float* Hbar, void* O,
                                                 void* workspace, size_t ws_bytes,
                                                 int64_t wait_ns, int32_t* status, void* stream);
+
+/* ---------------------------------------------------------------------------------
+ * Calls around the block attention. (No counterpart in the pages: a diffusion
+ * transformer's block also projects its tokens, rotates q and k by their positions and
+ * attends to an encoder's states.) They share the conventions at the top of this file
+ * but for the shapes: tensors are [Bt, H, L, d] with the head dimension contiguous and
+ * any batch, head and row strides. */
+
+/* Strides of a [Bt, H, L, d] tensor in elements. Every stride is >= 0 and, where its
+ * dimension is larger than 1, a multiple of 16 bytes (else BSA_ERR_UNSUPPORTED). A NULL
+ * pointer means contiguous. A projection's [Bt, L, H, d] is {L*H*d, d, H*d}. */
+typedef struct {
+  int64_t batch;
+  int64_t head;
+  int64_t row;
+} bsa_strides;
+
+typedef enum {
+  BSA_TYPE_BF16 = 0,
+  BSA_TYPE_FP16 = 1,
+  BSA_TYPE_FP32 = 2
+} bsa_type;
+
+/* Which two components of an axis's section of d turn together: 2i and 2i + 1, or i and
+ * i + (section / 2). */
+typedef enum {
+  BSA_PAIR_ADJACENT = 0,
+  BSA_PAIR_HALVES = 1
+} bsa_pairing;
+
+/* bsa_rotary — rotary positions with one to four axes (time, height, width of a video's
+ * or an image's tokens) on queries or keys, before bsa_precompute / bsa_route /
+ * bsa_forward.
+ *   The head dimension is cut into consecutive sections of axis_dim[0], axis_dim[1], ...
+ *   components, one per axis; what is left of d is copied. Pair i of axis a turns by
+ *     phi = pos[t][a] * base^(-2 i / axis_dim[a]):
+ *     y_lo = x_lo cos phi - x_hi sin phi,   y_hi = x_lo sin phi + x_hi cos phi.
+ *   inverse nonzero turns by -phi: the transposed map, which takes a gradient of y to
+ *   the gradient of x.
+ *   X, Y     [Bt, H, L, d] of `type` (bf16, fp16 or fp32), with strides xs, ys. Y may be
+ *            X with the same strides (in place); any other overlap is undefined;
+ *   d        a multiple of 8, at most 256;
+ *   pos      device fp32 [L, n_axes], or [Bt, L, n_axes] with pos_per_batch nonzero; a
+ *            text token at position 0 of every axis is left as it is. Angles are reduced
+ *            in 64 bits: positions of any size a float holds exactly are turned exactly.
+ *            A position that is not finite makes its token's rotated components NaN;
+ *   axis_dim host int32[n_axes], each even and >= 2, their sum at most d; 1 <= n_axes <= 4;
+ *   base     > 1, finite.
+ * Arithmetic is fp32, rounded once to `type`. */
+BSA_API bsa_status bsa_rotary(const void* X, const bsa_strides* xs, void* Y,
+                              const bsa_strides* ys, int32_t type, int32_t Bt, int32_t H,
+                              int32_t L, int32_t d, const float* pos, int32_t pos_per_batch,
+                              int32_t n_axes, const int32_t* axis_dim, double base,
+                              int32_t pairing, int32_t inverse, void* stream);
 
 #ifdef __cplusplus
 }

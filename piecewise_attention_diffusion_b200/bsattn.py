@@ -24,12 +24,15 @@ OK, ERR_INVALID_ARG, ERR_UNSUPPORTED, ERR_CUDA, ERR_BAD_CSR, ERR_TIMEOUT, ERR_WO
     ERR_CAPACITY, ERR_SCRATCH_LIMIT, ERR_BAD_PADDING = range(10)
 NOALLOC_SCRATCH_BYTES = 16 << 20
 MODE_KEEP_OR_DROP, MODE_PISA, MODE_PISA_BLOCK = 0, 1, 2
+TYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+PAIR_ADJACENT, PAIR_HALVES = 0, 1
 CALL_BUILD_MASK, CALL_PRECOMPUTE, CALL_ROUTE, CALL_FORWARD = 0, 1, 2, 3
 
 # Every symbol include/bsattn.h declares, in header order.
 EXPORTS = ("bsa_version", "bsa_status_string", "bsa_mask_blocks", "bsa_workspace_bytes",
            "bsa_build_mask", "bsa_precompute", "bsa_route", "bsa_forward",
-           "bsa_forward_noalloc", "bsa_selftest_wait_timeout", "bsa_selftest_forward_timeout")
+           "bsa_forward_noalloc", "bsa_selftest_wait_timeout", "bsa_selftest_forward_timeout",
+           "bsa_rotary")
 
 
 class BsaError(RuntimeError):
@@ -44,9 +47,14 @@ class MaskDesc(ctypes.Structure):
                 ("global_stride", ctypes.c_int32), ("global_rows_full", ctypes.c_int32)]
 
 
+class Strides(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int64), ("head", ctypes.c_int64), ("row", ctypes.c_int64)]
+
+
 _lib = None
 _vp, _i32, _i64, _f32, _sz = (ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64,
                               ctypes.c_float, ctypes.c_size_t)
+_sp = ctypes.POINTER(Strides)
 _SIGS = {
     "bsa_version": (_i32, []),
     "bsa_status_string": (ctypes.c_char_p, [_i32]),
@@ -65,6 +73,8 @@ _SIGS = {
     "bsa_selftest_forward_timeout": (_i32, [_vp, _vp, _vp, _i32, _i32, _i32, _i32, _i32, _vp,
                                             _vp, _i64, _i32, _vp, _vp, _vp, _vp, _vp, _sz,
                                             _i64, _vp, _vp]),
+    "bsa_rotary": (_i32, [_vp, _sp, _vp, _sp, _i32, _i32, _i32, _i32, _i32, _vp, _i32, _i32,
+                          ctypes.POINTER(_i32), ctypes.c_double, _i32, _i32, _vp]),
 }
 
 
@@ -274,6 +284,58 @@ def bsa_selftest_forward_timeout(Q, K, V, block, row_ptr, col_idx, mode, kbar, v
         "bsa_selftest_forward_timeout")
 
 
+# The calls around the block attention take strided tensors of several types; they run on
+# the tensors' device, whichever device is current.
+def _strided(t, name, dtype=None, shape=None):
+    """Check a [Bt, H, L, d] tensor whose last dimension is contiguous; its strides."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dim() != 4 or (shape is not None and tuple(t.shape) != tuple(shape)):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected "
+                         f"{'[Bt, H, L, d]' if shape is None else tuple(shape)}")
+    if t.dtype not in TYPES or (dtype is not None and t.dtype != dtype):
+        raise ValueError(f"{name} must be {dtype or 'bfloat16, float16 or float32'}, "
+                         f"got {t.dtype}")
+    if t.stride(3) != 1 and t.shape[3] > 1:
+        raise ValueError(f"{name}'s last dimension must be contiguous")
+    return Strides(t.stride(0), t.stride(1), t.stride(2))
+
+
+def _same_device(first, **others):
+    for name, t in others.items():
+        if t is not None and t.device != first.device:
+            raise ValueError(f"{name} is on {t.device}, expected {first.device}")
+
+
+def _call(fn, device, stream, *args):
+    """lib().fn(*args, stream) with `device` current; its current stream where none is given."""
+    if stream is None:
+        stream = torch.cuda.current_stream(device)
+    elif stream.device != device:
+        raise ValueError(f"the stream is on {stream.device}, the tensors on {device}")
+    f = getattr(lib(), fn)
+    if device.index == torch.cuda.current_device():
+        _check(f(*args, ctypes.c_void_p(stream.cuda_stream)), fn)
+    else:
+        with torch.cuda.device(device):
+            _check(f(*args, ctypes.c_void_p(stream.cuda_stream)), fn)
+
+
+def bsa_rotary(X, Y, pos, axis_dims, base=10000.0, pairing=PAIR_ADJACENT, inverse=False,
+               stream=None):
+    xs = _strided(X, "X")
+    ys = _strided(Y, "Y", X.dtype, X.shape)
+    Bt, H, L, d = X.shape
+    n = len(axis_dims)
+    _need(pos, torch.float32, "pos", (Bt, L, n) if pos.dim() == 3 else (L, n))
+    _same_device(X, Y=Y, pos=pos)
+    dims = (_i32 * max(n, 1))(*[int(a) for a in axis_dims])
+    _call("bsa_rotary", X.device, stream, _ptr(X), xs, _ptr(Y), ys, TYPES[X.dtype], Bt, H, L, d,
+          _ptr(pos), int(pos.dim() == 3), n, dims, float(base), int(pairing), int(inverse))
+
+
 # ------------------------------------------------------------ allocating helpers
 def workspace(call, Bt, H, L, d, block, device="cuda"):
     n = bsa_workspace_bytes(call, Bt, H, L, d, block)
@@ -332,6 +394,18 @@ def forward(Q, K, V, block, row_ptr, col_idx, csr_per_head, mode, stats=None, sc
     bsa_forward(Q, K, V, block, row_ptr, col_idx, csr_per_head, mode, st.get("kbar"),
                 st.get("vsum"), st.get("Hbar"), scale, O, lse, ws, status, key_valid=key_valid)
     return O, lse
+
+
+def rotary(X, pos, axis_dims, base=10000.0, pairing=PAIR_ADJACENT, inverse=False, out=None,
+           stream=None):
+    """Rotary positions on [Bt, H, L, d] queries or keys (any strides, such as a projection's
+    [Bt, L, H, d] transposed): fp32 pos [L, n] or [Bt, L, n], one column per axis, whose
+    sections of d are axis_dims. Returns a contiguous [Bt, H, L, d], or `out` (which may be X
+    itself). inverse turns back, which also takes gradients through the rotation."""
+    if out is None:
+        out = torch.empty(X.shape, dtype=X.dtype, device=X.device)
+    bsa_rotary(X, out, pos, axis_dims, base, pairing, inverse, stream=stream)
+    return out
 
 
 def default_scale(d: int) -> float:

@@ -44,6 +44,25 @@ int mask_blocks(const bsa_mask_desc* d) {
   return (int)m;
 }
 
+// The strides of a [Bt, H, L, d] tensor: as given, or contiguous where there are none. A
+// dimension of size 1 is never stepped over, so its stride becomes 0.
+bsa_strides strides_of(const bsa_strides* s, int Bt, int H, int L, int d) {
+  bsa_strides r = s != nullptr ? *s : bsa_strides{(int64_t)H * L * d, (int64_t)L * d, d};
+  if (Bt == 1) r.batch = 0;
+  if (H == 1) r.head = 0;
+  if (L == 1) r.row = 0;
+  return r;
+}
+
+// Whole 16-byte steps, and no step or sum of steps that could pass 2^62 bytes.
+bsa_status check_strides(const bsa_strides& s, int elem_bytes) {
+  for (const int64_t v : {s.batch, s.head, s.row}) {
+    if (v < 0 || v >= (int64_t)1 << 40) return BSA_ERR_INVALID_ARG;
+    if (v * elem_bytes % 16 != 0) return BSA_ERR_UNSUPPORTED;
+  }
+  return BSA_OK;
+}
+
 }  // namespace
 
 namespace bsa {
@@ -97,7 +116,7 @@ bsa_status check_forward_args(const ForwardArgs& a) {
 
 extern "C" {
 
-int32_t bsa_version(void) { return 110; }
+int32_t bsa_version(void) { return 200; }
 
 const char* bsa_status_string(int32_t code) {
   switch (code) {
@@ -203,6 +222,39 @@ bsa_status bsa_selftest_forward_timeout(const void* Q, const void* K, const void
   if (!workspace_ok(bsa::forward_workspace(a.s), workspace, ws_bytes)) return BSA_ERR_WORKSPACE;
   a.wait_ns = static_cast<uint64_t>(wait_ns);
   return from_cuda(bsa::launch_forward(a, static_cast<cudaStream_t>(stream)));
+}
+
+bsa_status bsa_rotary(const void* X, const bsa_strides* xs, void* Y, const bsa_strides* ys,
+                      int32_t type, int32_t Bt, int32_t H, int32_t L, int32_t d,
+                      const float* pos, int32_t pos_per_batch, int32_t n_axes,
+                      const int32_t* axis_dim, double base, int32_t pairing, int32_t inverse,
+                      void* stream) {
+  if (!X || !Y || !pos || !axis_dim) return BSA_ERR_INVALID_ARG;
+  if (Bt <= 0 || H <= 0 || L <= 0 || d <= 0) return BSA_ERR_INVALID_ARG;
+  if (type != BSA_TYPE_BF16 && type != BSA_TYPE_FP16 && type != BSA_TYPE_FP32)
+    return BSA_ERR_INVALID_ARG;
+  if (pairing != BSA_PAIR_ADJACENT && pairing != BSA_PAIR_HALVES) return BSA_ERR_INVALID_ARG;
+  if (n_axes < 1 || n_axes > 4 || !(base > 1.0) || !(base <= 1e30)) return BSA_ERR_INVALID_ARG;
+  if (d % 8 != 0 || d > 256) return BSA_ERR_UNSUPPORTED;
+  if (H > 65535 || (int64_t)Bt * L > INT32_MAX) return BSA_ERR_UNSUPPORTED;
+  int64_t turned = 0;
+  for (int i = 0; i < n_axes; ++i) {
+    if (axis_dim[i] < 2 || axis_dim[i] % 2 != 0) return BSA_ERR_INVALID_ARG;
+    turned += axis_dim[i];
+  }
+  if (turned > d) return BSA_ERR_INVALID_ARG;
+  if (!aligned16(X) || !aligned16(Y) || (reinterpret_cast<uintptr_t>(pos) & 3u) != 0)
+    return BSA_ERR_INVALID_ARG;
+  const bsa::RotaryArgs a{X, strides_of(xs, Bt, H, L, d), Y, strides_of(ys, Bt, H, L, d), type, Bt,
+                          H, L, d, pos, pos_per_batch, n_axes, axis_dim, base, pairing, inverse};
+  const int elem = type == BSA_TYPE_FP32 ? 4 : 2;
+  bsa_status r = check_strides(a.xs, elem);
+  if (r == BSA_OK) r = check_strides(a.ys, elem);
+  if (r != BSA_OK) return r;
+  // a step of 0 would have several threads write one place
+  if ((Bt > 1 && a.ys.batch == 0) || (H > 1 && a.ys.head == 0) || (L > 1 && a.ys.row == 0))
+    return BSA_ERR_INVALID_ARG;
+  return from_cuda(bsa::launch_rotary(a, static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

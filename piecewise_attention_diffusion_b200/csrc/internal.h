@@ -77,4 +77,18 @@ cudaError_t launch_forward_tc(const ForwardArgs& a, const int32_t* flag, cudaStr
 cudaError_t launch_forward_pair(const ForwardArgs& a, const int32_t* flag, const void* kb16,
                                 const void* vs16, const void* hb16, int Mp, cudaStream_t st);
 
+struct RotaryArgs {
+  const void* X;
+  bsa_strides xs;
+  void* Y;
+  bsa_strides ys;
+  int type, Bt, H, L, d;
+  const float* pos;
+  int pos_per_batch, n_axes;
+  const int32_t* axis_dim;
+  double base;
+  int pairing, inverse;
+};
+cudaError_t launch_rotary(const RotaryArgs& a, cudaStream_t st);
+
 }  // namespace bsa

@@ -1,0 +1,201 @@
+// bsa_rotary: rotary positions with up to four axes on a [Bt, H, L, d] tensor.
+//
+// Every pair (x_lo, x_hi) of components turns by phi = pos[axis] * base^(-2 i / axis_dim):
+//     y_lo = x_lo cos phi - x_hi sin phi,   y_hi = x_lo sin phi + x_hi cos phi.
+// phi depends on the token and the pair, not on the head, so a thread takes W pairs of one
+// token, forms their sines and cosines once, and walks over a group of heads: per head it
+// loads its components, turns them and stores them. The kernel reads x and writes y once
+// and is bound by memory; kUnroll heads are loaded before the first is turned, which is
+// what keeps enough bytes in flight.
+//
+// The angle is formed in 64 bits as a number of turns, pos * base^(-2 i / axis_dim) / 2 pi,
+// whose whole part is dropped before rounding to fp32: in 32 bits the angle of position
+// 16384 would already be off by 1e-3.
+#include <math.h>
+
+#include <algorithm>
+
+#include "common.cuh"
+#include "internal.h"
+#include "types.cuh"
+
+namespace bsa {
+namespace rotary {
+
+constexpr int kThreads = 256;
+constexpr int kMaxPairs = 128;  // d <= 256
+constexpr int kUnroll = 4;      // heads in flight per thread
+constexpr int kCopy = 255;      // axis of the components that no axis turns
+
+struct Params {
+  const void* x;
+  void* y;
+  bsa_strides xs, ys;
+  const float* pos;
+  int Bt, H, L, n_axes, pos_per_batch, heads_per_cta;
+  int groups;  // threads per token: pairs / W
+  int64_t n;   // threads in all: Bt * L * groups
+  float sign;
+  // of every pair: turns per unit of position, axis, first and second component
+  double rate[kMaxPairs];
+  uint8_t axis[kMaxPairs], lo[kMaxPairs], hi[kMaxPairs];
+};
+
+// W pairs per thread. kAdjacent: 2W consecutive components; else W consecutive first
+// components and W consecutive second ones (the host chose W so that neither run crosses
+// a section).
+template <typename T, int W, bool kAdjacent>
+__global__ void __launch_bounds__(kThreads)
+k_rotary(const __grid_constant__ Params p) {
+  // the pair tables, from the parameters (whose reads are serial where lanes differ)
+  __shared__ double rate_s[kMaxPairs];
+  __shared__ uint8_t axis_s[kMaxPairs];
+  const int pairs = p.groups * W;
+  for (int i = threadIdx.x; i < pairs; i += kThreads) {
+    rate_s[i] = p.rate[i];
+    axis_s[i] = p.axis[i];
+  }
+  __syncthreads();
+  const int64_t id = (int64_t)blockIdx.x * kThreads + threadIdx.x;
+  if (id >= p.n) return;
+  const int g = (int)(id % p.groups);
+  const int64_t token = id / p.groups;
+  const int t = (int)(token % p.L), b = (int)(token / p.L);
+  const float* pos = p.pos + ((p.pos_per_batch ? (int64_t)b * p.L : 0) + t) * p.n_axes;
+
+  float c[W], s[W];
+  bool copy[W];
+#pragma unroll
+  for (int j = 0; j < W; ++j) {
+    const int axis = axis_s[g * W + j];
+    copy[j] = axis == kCopy;
+    c[j] = 1.f;
+    s[j] = 0.f;
+    if (!copy[j]) {
+      double turns = (double)__ldg(pos + axis) * rate_s[g * W + j];
+      turns -= rint(turns);
+      sincospif((float)(2.0 * turns), &s[j], &c[j]);
+      s[j] *= p.sign;
+    }
+  }
+  const int lo = p.lo[g * W], hi = p.hi[g * W];
+  const int h0 = blockIdx.y * p.heads_per_cta;
+  const int h1 = min(h0 + p.heads_per_cta, p.H);
+  const T* x = static_cast<const T*>(p.x) + b * p.xs.batch + t * p.xs.row + h0 * p.xs.head;
+  T* y = static_cast<T*>(p.y) + b * p.ys.batch + t * p.ys.row + h0 * p.ys.head;
+
+  for (int h = h0; h < h1; h += kUnroll) {
+    Pack<T, W> first[kUnroll], second[kUnroll];
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u)
+      if (h + u < h1) {
+        const T* row = x + u * p.xs.head;
+        if (kAdjacent) {
+          const Pack<T, 2 * W> v = *reinterpret_cast<const Pack<T, 2 * W>*>(row + lo);
+#pragma unroll
+          for (int j = 0; j < W; ++j) {
+            first[u].v[j] = v.v[2 * j];
+            second[u].v[j] = v.v[2 * j + 1];
+          }
+        } else {
+          first[u] = *reinterpret_cast<const Pack<T, W>*>(row + lo);
+          second[u] = *reinterpret_cast<const Pack<T, W>*>(row + hi);
+        }
+      }
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u)
+      if (h + u < h1) {
+        T* row = y + u * p.ys.head;
+        Pack<T, W> a = first[u], d = second[u];
+#pragma unroll
+        for (int j = 0; j < W; ++j) {
+          const float xa = to_f32(first[u].v[j]), xb = to_f32(second[u].v[j]);
+          // copied components are not multiplied: an infinity stays one
+          if (!copy[j]) {
+            a.v[j] = from_f32<T>(xa * c[j] - xb * s[j]);
+            d.v[j] = from_f32<T>(xa * s[j] + xb * c[j]);
+          }
+        }
+        if (kAdjacent) {
+          Pack<T, 2 * W> v;
+#pragma unroll
+          for (int j = 0; j < W; ++j) {
+            v.v[2 * j] = a.v[j];
+            v.v[2 * j + 1] = d.v[j];
+          }
+          *reinterpret_cast<Pack<T, 2 * W>*>(row + lo) = v;
+        } else {
+          *reinterpret_cast<Pack<T, W>*>(row + lo) = a;
+          *reinterpret_cast<Pack<T, W>*>(row + hi) = d;
+        }
+      }
+    x += kUnroll * p.xs.head;
+    y += kUnroll * p.ys.head;
+  }
+}
+
+template <typename T, int W, bool kAdjacent>
+cudaError_t run(Params& p, cudaStream_t st) {
+  int pairs = 0;
+  while (pairs < kMaxPairs && p.axis[pairs] != 254) ++pairs;
+  p.groups = pairs / W;
+  p.n = (int64_t)p.Bt * p.L * p.groups;
+  const int64_t ctas = (p.n + kThreads - 1) / kThreads;
+  // all heads in one thread share its sines; fewer per thread where that leaves the card
+  // short of CTAs
+  const int64_t want = 148 * 8;
+  int split = (int)std::min<int64_t>(ceil_div(p.H, kUnroll), (want + ctas - 1) / ctas);
+  p.heads_per_cta = ceil_div(ceil_div(p.H, split), kUnroll) * kUnroll;
+  const dim3 grid((unsigned)ctas, (unsigned)ceil_div(p.H, p.heads_per_cta));
+  k_rotary<T, W, kAdjacent><<<grid, kThreads, 0, st>>>(p);
+  return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t dispatch(Params& p, int pairing, int width, cudaStream_t st) {
+  if (pairing == BSA_PAIR_ADJACENT) return run<T, 4, true>(p, st);
+  if (width == 8) return run<T, 8, false>(p, st);
+  if (width == 4) return run<T, 4, false>(p, st);
+  if (width == 2) return run<T, 2, false>(p, st);
+  return run<T, 1, false>(p, st);
+}
+
+}  // namespace rotary
+
+cudaError_t launch_rotary(const RotaryArgs& a, cudaStream_t st) {
+  rotary::Params p;
+  p.x = a.X;
+  p.y = a.Y;
+  p.xs = a.xs;
+  p.ys = a.ys;
+  p.pos = a.pos;
+  p.Bt = a.Bt;
+  p.H = a.H;
+  p.L = a.L;
+  p.n_axes = a.n_axes;
+  p.pos_per_batch = a.pos_per_batch != 0;
+  p.sign = a.inverse ? -1.f : 1.f;
+  // the sections of d: one per axis, then the components that are copied
+  int n = 0, begin = 0, rest = 0, width = 8;
+  for (int i = 0; i < a.n_axes; ++i) rest += a.axis_dim[i];
+  rest = a.d - rest;
+  for (int i = 0; i <= a.n_axes; ++i) {
+    const int dim = i < a.n_axes ? a.axis_dim[i] : rest;
+    const int half = dim / 2;
+    while (half % width != 0) width /= 2;
+    for (int j = 0; j < half; ++j, ++n) {
+      p.axis[n] = (uint8_t)(i < a.n_axes ? i : rotary::kCopy);
+      p.rate[n] = i < a.n_axes ? pow(a.base, -2.0 * j / dim) / (2.0 * M_PI) : 0.0;
+      const bool adj = a.pairing == BSA_PAIR_ADJACENT;
+      p.lo[n] = (uint8_t)(begin + (adj ? 2 * j : j));
+      p.hi[n] = (uint8_t)(begin + (adj ? 2 * j + 1 : j + half));
+    }
+    begin += dim;
+  }
+  if (n < rotary::kMaxPairs) p.axis[n] = 254;  // end of the table
+  if (a.type == BSA_TYPE_BF16) return rotary::dispatch<__nv_bfloat16>(p, a.pairing, width, st);
+  if (a.type == BSA_TYPE_FP16) return rotary::dispatch<__half>(p, a.pairing, width, st);
+  return rotary::dispatch<float>(p, a.pairing, width, st);
+}
+
+}  // namespace bsa
