@@ -332,6 +332,47 @@ BSA_API bsa_status bsa_rotary(const void* X, const bsa_strides* xs, void* Y,
                               int32_t n_axes, const int32_t* axis_dim, double base,
                               int32_t pairing, int32_t inverse, void* stream);
 
+typedef enum {
+  BSA_ACT_NONE = 0,
+  BSA_ACT_GELU_TANH = 1, /* z (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))) / 2 */
+  BSA_ACT_GELU_ERF = 2,  /* z (1 + erf(z / sqrt 2)) / 2                      */
+  BSA_ACT_SILU = 3       /* z / (1 + e^-z)                                    */
+} bsa_act;
+
+/* Bytes of device workspace bsa_linear needs; 0 if none. */
+BSA_API size_t bsa_linear_workspace_bytes(int32_t Bt, int32_t L, int32_t K, int32_t N);
+
+/* bsa_linear — matrix product with bias, activation, gate and residual:
+ *     Y[b, t, n] = R[b, t, n] + gate[b, n] * act(sum_k X[b, t, k] W[n, k] + bias[n]).
+ * The projections into and out of the attention, the feed-forward and the modulation
+ * layers. X's K columns and Y's N columns may be cut into heads, so that a projection
+ * writes the [Bt, H, L, d] that bsa_precompute / bsa_route / bsa_forward read, and the
+ * output projection reads the O that bsa_forward writes.
+ *   X        `type` [Bt, x_heads, L, K / x_heads] with strides xs, 16-byte aligned;
+ *            x_heads 1: plain [Bt, L, K]. With x_heads > 1, K / x_heads is a multiple of
+ *            64. A batch or head stride of 0 repeats one tensor; the row stride is not 0
+ *            (unless L is 1);
+ *   W        `type` [N, K], rows w_row elements apart (0: K), w_row a multiple of 8;
+ *            16-byte aligned;
+ *   bias     nullable `type` [N];   gate  nullable `type` [Bt, N], contiguous;
+ *   R        nullable `type` [Bt, y_heads, L, N / y_heads] with strides rs, any (a stride
+ *            of 0 repeats);
+ *   Y        `type`, the shape of R, strides ys: any that step over no place twice (with
+ *            bases and strides of whole 16 bytes it is written by TMA); with y_heads > 1,
+ *            N / y_heads is a multiple of 64. Y may be R with the same strides; it must
+ *            not overlap the other inputs;
+ *   type     bf16 or fp16; sums are fp32, rounded once after the residual;
+ *   workspace  device, >= bsa_linear_workspace_bytes(Bt, L, K, N) bytes, contents scratch
+ *            (NULL and 0 where that is 0);
+ *   status   see the conventions (BSA_ERR_TIMEOUT).
+ * Results are the same bits on every run on one kind of GPU: no atomics. */
+BSA_API bsa_status bsa_linear(const void* X, const bsa_strides* xs, int32_t x_heads,
+                              const void* W, int64_t w_row, const void* bias, int32_t act,
+                              const void* gate, const void* R, const bsa_strides* rs, void* Y,
+                              const bsa_strides* ys, int32_t y_heads, int32_t type, int32_t Bt,
+                              int32_t L, int32_t K, int32_t N, void* workspace,
+                              size_t ws_bytes, int32_t* status, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

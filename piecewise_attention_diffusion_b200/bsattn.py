@@ -26,13 +26,14 @@ NOALLOC_SCRATCH_BYTES = 16 << 20
 MODE_KEEP_OR_DROP, MODE_PISA, MODE_PISA_BLOCK = 0, 1, 2
 TYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 PAIR_ADJACENT, PAIR_HALVES = 0, 1
+ACT_NONE, ACT_GELU_TANH, ACT_GELU_ERF, ACT_SILU = range(4)
 CALL_BUILD_MASK, CALL_PRECOMPUTE, CALL_ROUTE, CALL_FORWARD = 0, 1, 2, 3
 
 # Every symbol include/bsattn.h declares, in header order.
 EXPORTS = ("bsa_version", "bsa_status_string", "bsa_mask_blocks", "bsa_workspace_bytes",
            "bsa_build_mask", "bsa_precompute", "bsa_route", "bsa_forward",
            "bsa_forward_noalloc", "bsa_selftest_wait_timeout", "bsa_selftest_forward_timeout",
-           "bsa_rotary")
+           "bsa_rotary", "bsa_linear_workspace_bytes", "bsa_linear")
 
 
 class BsaError(RuntimeError):
@@ -75,6 +76,9 @@ _SIGS = {
                                             _i64, _vp, _vp]),
     "bsa_rotary": (_i32, [_vp, _sp, _vp, _sp, _i32, _i32, _i32, _i32, _i32, _vp, _i32, _i32,
                           ctypes.POINTER(_i32), ctypes.c_double, _i32, _i32, _vp]),
+    "bsa_linear_workspace_bytes": (_sz, [_i32, _i32, _i32, _i32]),
+    "bsa_linear": (_i32, [_vp, _sp, _i32, _vp, _i64, _vp, _i32, _vp, _vp, _sp, _vp, _sp, _i32,
+                          _i32, _i32, _i32, _i32, _i32, _vp, _sz, _vp, _vp]),
 }
 
 
@@ -286,54 +290,115 @@ def bsa_selftest_forward_timeout(Q, K, V, block, row_ptr, col_idx, mode, kbar, v
 
 # The calls around the block attention take strided tensors of several types; they run on
 # the tensors' device, whichever device is current.
-def _strided(t, name, dtype=None, shape=None):
-    """Check a [Bt, H, L, d] tensor whose last dimension is contiguous; its strides."""
+def _strided(t, name, first=None, shape=None):
+    """Check a [Bt, H, L, d] tensor (or [Bt, L, N] for a single head) whose last dimension is
+    contiguous, of `first`'s type and device; its strides."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    if t.dim() != 4 or (shape is not None and tuple(t.shape) != tuple(shape)):
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected "
-                         f"{'[Bt, H, L, d]' if shape is None else tuple(shape)}")
-    if t.dtype not in TYPES or (dtype is not None and t.dtype != dtype):
-        raise ValueError(f"{name} must be {dtype or 'bfloat16, float16 or float32'}, "
-                         f"got {t.dtype}")
-    if t.stride(3) != 1 and t.shape[3] > 1:
+    if first is not None and (t.dtype != first.dtype or t.device != first.device):
+        raise ValueError(f"{name} must be {first.dtype} on {first.device}, "
+                         f"got {t.dtype} on {t.device}")
+    if t.dtype not in TYPES:
+        raise ValueError(f"{name} must be bfloat16, float16 or float32, got {t.dtype}")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    st = t.stride()
+    if st[-1] != 1 and t.shape[-1] > 1:
         raise ValueError(f"{name}'s last dimension must be contiguous")
-    return Strides(t.stride(0), t.stride(1), t.stride(2))
+    if len(st) == 4:
+        return Strides(st[0], st[1], st[2])
+    if len(st) == 3:
+        return Strides(st[0], 0, st[1])
+    raise ValueError(f"{name} has shape {tuple(t.shape)}, expected [Bt, H, L, d]")
 
 
-def _same_device(first, **others):
-    for name, t in others.items():
-        if t is not None and t.device != first.device:
-            raise ValueError(f"{name} is on {t.device}, expected {first.device}")
+def _plain(t, dtype, name, shape, device):
+    """The address of a contiguous tensor of this type and shape on `device`; None for None."""
+    if t is None:
+        return None
+    _need(t, dtype, name, shape)
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    return t.data_ptr()
+
+
+def _status_ptr(status, device):
+    return _plain(status, torch.int32, "status", (1,), device)
 
 
 def _call(fn, device, stream, *args):
-    """lib().fn(*args, stream) with `device` current; its current stream where none is given."""
+    """lib().fn(*args, stream) with `device` current; on its current stream if none is given."""
     if stream is None:
-        stream = torch.cuda.current_stream(device)
+        raw = torch._C._cuda_getCurrentRawStream(device.index)
     elif stream.device != device:
         raise ValueError(f"the stream is on {stream.device}, the tensors on {device}")
+    else:
+        raw = stream.cuda_stream
     f = getattr(lib(), fn)
     if device.index == torch.cuda.current_device():
-        _check(f(*args, ctypes.c_void_p(stream.cuda_stream)), fn)
+        _check(f(*args, raw), fn)
     else:
         with torch.cuda.device(device):
-            _check(f(*args, ctypes.c_void_p(stream.cuda_stream)), fn)
+            _check(f(*args, raw), fn)
 
 
 def bsa_rotary(X, Y, pos, axis_dims, base=10000.0, pairing=PAIR_ADJACENT, inverse=False,
                stream=None):
     xs = _strided(X, "X")
-    ys = _strided(Y, "Y", X.dtype, X.shape)
     Bt, H, L, d = X.shape
+    ys = xs if Y is X else _strided(Y, "Y", X, X.shape)
     n = len(axis_dims)
-    _need(pos, torch.float32, "pos", (Bt, L, n) if pos.dim() == 3 else (L, n))
-    _same_device(X, Y=Y, pos=pos)
-    dims = (_i32 * max(n, 1))(*[int(a) for a in axis_dims])
-    _call("bsa_rotary", X.device, stream, _ptr(X), xs, _ptr(Y), ys, TYPES[X.dtype], Bt, H, L, d,
-          _ptr(pos), int(pos.dim() == 3), n, dims, float(base), int(pairing), int(inverse))
+    per = pos.dim() == 3
+    pos_ptr = _plain(pos, torch.float32, "pos", (Bt, L, n) if per else (L, n), X.device)
+    _call("bsa_rotary", X.device, stream, X.data_ptr(), xs, Y.data_ptr(), ys, TYPES[X.dtype], Bt,
+          H, L, d, pos_ptr, per, n, (_i32 * max(n, 1))(*axis_dims), base, pairing, bool(inverse))
+
+
+def bsa_linear_workspace_bytes(Bt: int, L: int, K: int, N: int) -> int:
+    return int(lib().bsa_linear_workspace_bytes(Bt, L, K, N))
+
+
+def _linear_shape(X, W, y_heads):
+    """(Bt, L, K, N, x_heads) of X [Bt, L, K] or [Bt, H, L, d] and W [N, K]."""
+    if not isinstance(W, torch.Tensor) or W.dim() != 2:
+        raise ValueError("W must be a [N, K] tensor")
+    Bt, L = X.shape[0], X.shape[-2]
+    x_heads = X.shape[1] if X.dim() == 4 else 1
+    N, K = W.shape
+    if K != x_heads * X.shape[-1]:
+        raise ValueError(f"W has shape {tuple(W.shape)}, X {tuple(X.shape)}")
+    if y_heads and N % y_heads:
+        raise ValueError(f"{N} columns do not divide into {y_heads} heads")
+    return Bt, L, K, N, x_heads
+
+
+def bsa_linear(X, W, Y, bias=None, act=ACT_NONE, gate=None, R=None, workspace=None, status=None,
+               stream=None):
+    xs = _strided(X, "X")
+    ys = _strided(Y, "Y", X)
+    y_heads = Y.shape[1] if Y.dim() == 4 else 1
+    Bt, L, K, N, x_heads = _linear_shape(X, W, y_heads)
+    want = (Bt, y_heads, L, N // y_heads) if Y.dim() == 4 else (Bt, L, N)
+    if Y.shape != want:
+        raise ValueError(f"Y has shape {tuple(Y.shape)}, expected {want}")
+    dev, dtype = X.device, X.dtype
+    if not W.is_cuda or W.dtype != dtype or W.device != dev:
+        raise ValueError(f"W must be {dtype} on {dev}, got {W.dtype} on {W.device}")
+    if W.stride(1) != 1 and K > 1:
+        raise ValueError("W's rows must be contiguous")
+    rs = None if R is None else ys if R is Y else _strided(R, "R", X, Y.shape)
+    ws_bytes = 0
+    if workspace is not None:
+        if not workspace.is_cuda or workspace.device != dev:
+            raise ValueError(f"workspace must be on {dev}")
+        ws_bytes = workspace.numel() * workspace.element_size()
+    _call("bsa_linear", dev, stream, X.data_ptr(), xs, x_heads, W.data_ptr(),
+          W.stride(0) if N > 1 else 0, _plain(bias, dtype, "bias", (N,), dev), act,
+          _plain(gate, dtype, "gate", (Bt, N), dev), None if R is None else R.data_ptr(), rs,
+          Y.data_ptr(), ys, y_heads, TYPES[dtype], Bt, L, K, N, _ptr(workspace), ws_bytes,
+          _status_ptr(status, dev))
 
 
 # ------------------------------------------------------------ allocating helpers
@@ -403,8 +468,24 @@ def rotary(X, pos, axis_dims, base=10000.0, pairing=PAIR_ADJACENT, inverse=False
     sections of d are axis_dims. Returns a contiguous [Bt, H, L, d], or `out` (which may be X
     itself). inverse turns back, which also takes gradients through the rotation."""
     if out is None:
-        out = torch.empty(X.shape, dtype=X.dtype, device=X.device)
+        out = X.new_empty(X.shape)
     bsa_rotary(X, out, pos, axis_dims, base, pairing, inverse, stream=stream)
+    return out
+
+
+def linear(X, W, bias=None, act=ACT_NONE, gate=None, residual=None, heads=0, status=None, ws=None,
+           out=None, stream=None):
+    """residual + gate * act(X W^T + bias): X [Bt, L, K], or [Bt, H, L, d] whose heads side by
+    side are the K columns; W [N, K]; gate [Bt, N]. Returns [Bt, L, N], with `heads` the
+    [Bt, heads, L, N / heads] that the attention takes, or `out` (which may be the residual)."""
+    if out is None:
+        Bt, L, K, N, _ = _linear_shape(X, W, heads)
+        out = X.new_empty((Bt, heads, L, N // heads) if heads else (Bt, L, N))
+    if ws is None:
+        need = bsa_linear_workspace_bytes(X.shape[0], X.shape[-2], W.shape[1], W.shape[0])
+        if need:
+            ws = torch.empty(need, dtype=torch.uint8, device=X.device)
+    bsa_linear(X, W, out, bias, act, gate, residual, ws, status, stream)
     return out
 
 

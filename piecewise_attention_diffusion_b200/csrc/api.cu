@@ -257,4 +257,53 @@ bsa_status bsa_rotary(const void* X, const bsa_strides* xs, void* Y, const bsa_s
   return from_cuda(bsa::launch_rotary(a, static_cast<cudaStream_t>(stream)));
 }
 
+size_t bsa_linear_workspace_bytes(int32_t Bt, int32_t L, int32_t K, int32_t N) {
+  if (Bt <= 0 || L <= 0 || K <= 0 || N <= 0) return 0;
+  return bsa::linear_workspace(Bt, L, K, N);
+}
+
+bsa_status bsa_linear(const void* X, const bsa_strides* xs, int32_t x_heads, const void* W,
+                      int64_t w_row, const void* bias, int32_t act, const void* gate,
+                      const void* R, const bsa_strides* rs, void* Y, const bsa_strides* ys,
+                      int32_t y_heads, int32_t type, int32_t Bt, int32_t L, int32_t K, int32_t N,
+                      void* workspace, size_t ws_bytes, int32_t* status, void* stream) {
+  if (!X || !W || !Y) return BSA_ERR_INVALID_ARG;
+  if (Bt <= 0 || L <= 0 || K <= 0 || N <= 0 || x_heads <= 0 || y_heads <= 0)
+    return BSA_ERR_INVALID_ARG;
+  if (K % x_heads != 0 || N % y_heads != 0 || w_row < 0) return BSA_ERR_INVALID_ARG;
+  if (act < BSA_ACT_NONE || act > BSA_ACT_SILU) return BSA_ERR_INVALID_ARG;
+  if (type != BSA_TYPE_BF16 && type != BSA_TYPE_FP16)
+    return type == BSA_TYPE_FP32 ? BSA_ERR_UNSUPPORTED : BSA_ERR_INVALID_ARG;
+  if ((x_heads > 1 && K / x_heads % 64 != 0) || (y_heads > 1 && N / y_heads % 64 != 0))
+    return BSA_ERR_UNSUPPORTED;
+  // rows, columns and tiles are counted in 32 bits
+  if ((int64_t)Bt * L >= (int64_t)1 << 30 || K >= 1 << 30 || N >= 1 << 30)
+    return BSA_ERR_UNSUPPORTED;
+  if ((((int64_t)L + 255) / 256 * Bt) * (((int64_t)N + 63) / 64) >= INT32_MAX)
+    return BSA_ERR_UNSUPPORTED;
+  if (!aligned16(X) || !aligned16(W)) return BSA_ERR_INVALID_ARG;
+  for (const void* v : {bias, gate, R, static_cast<const void*>(Y)})
+    if ((reinterpret_cast<uintptr_t>(v) & 1u) != 0) return BSA_ERR_INVALID_ARG;
+  const bsa::LinearArgs a{X, strides_of(xs, Bt, x_heads, L, K / x_heads), x_heads, W,
+                          w_row == 0 ? K : w_row, bias, act, gate, R,
+                          strides_of(rs, Bt, y_heads, L, N / y_heads), Y,
+                          strides_of(ys, Bt, y_heads, L, N / y_heads), y_heads, type, Bt, L, K, N,
+                          workspace, status, 0};
+  if (a.w_row < K || a.w_row >= (int64_t)1 << 39) return BSA_ERR_INVALID_ARG;
+  if (N > 1 && a.w_row % 8 != 0) return BSA_ERR_UNSUPPORTED;
+  const bsa_status r = check_strides(a.xs, 2);
+  if (r != BSA_OK) return r;
+  if (a.xs.batch >= (int64_t)1 << 39 || a.xs.head >= (int64_t)1 << 39 ||
+      a.xs.row >= (int64_t)1 << 39)
+    return BSA_ERR_UNSUPPORTED;  // a tensor map's stride is below 2^40 bytes
+  if (L > 1 && a.xs.row == 0) return BSA_ERR_INVALID_ARG;
+  for (const int64_t v : {a.ys.batch, a.ys.head, a.ys.row, a.rs.batch, a.rs.head, a.rs.row})
+    if (v < 0 || v >= (int64_t)1 << 39) return BSA_ERR_INVALID_ARG;
+  if ((Bt > 1 && a.ys.batch == 0) || (y_heads > 1 && a.ys.head == 0) || (L > 1 && a.ys.row == 0))
+    return BSA_ERR_INVALID_ARG;
+  if (!workspace_ok(bsa::linear_workspace(Bt, L, K, N), workspace, ws_bytes))
+    return BSA_ERR_WORKSPACE;
+  return from_cuda(bsa::launch_linear(a, static_cast<cudaStream_t>(stream)));
+}
+
 }  // extern "C"

@@ -91,4 +91,25 @@ struct RotaryArgs {
 };
 cudaError_t launch_rotary(const RotaryArgs& a, cudaStream_t st);
 
+struct LinearArgs {
+  const void* X;
+  bsa_strides xs;
+  int x_heads;
+  const void* W;
+  int64_t w_row;
+  const void* bias;
+  int act;
+  const void* gate;
+  const void* R;
+  bsa_strides rs;
+  void* Y;
+  bsa_strides ys;
+  int y_heads, type, Bt, L, K, N;
+  void* ws;
+  int32_t* status;
+  int gate_rows;  // set at launch: rows that share one gate vector
+};
+size_t linear_workspace(int Bt, int L, int K, int N);
+cudaError_t launch_linear(const LinearArgs& a, cudaStream_t st);
+
 }  // namespace bsa

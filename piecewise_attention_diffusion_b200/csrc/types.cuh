@@ -22,6 +22,11 @@ __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float x) {
 template <>
 __device__ __forceinline__ __half from_f32<__half>(float x) { return __float2half_rn(x); }
 
+template <typename T>
+__host__ __device__ constexpr bool is_bf16() { return false; }
+template <>
+__host__ __device__ constexpr bool is_bf16<__nv_bfloat16>() { return true; }
+
 // N consecutive elements, loaded and stored as one or more words of up to 16 bytes.
 template <typename T, int N>
 struct alignas(sizeof(T) * N < 16 ? sizeof(T) * N : 16) Pack {

@@ -51,3 +51,36 @@ def test_bindings_refuse_host_tensors():
     x = torch.zeros(1, 2, 8, 64, dtype=torch.bfloat16)
     with pytest.raises(ValueError, match="CUDA"):
         b.rotary(x, torch.zeros(8, 1), (64,))
+
+
+def _linear(x=P, xs=None, xh=1, w=P, w_row=0, bias=None, act=0, gate=None, r=None, rs=None, y=P,
+            ys=None, yh=1, type=0, Bt=2, L=8, K=128, N=192, ws=P, ws_bytes=1 << 40, status=None):
+    return b.lib().bsa_linear(x, xs, xh, w, w_row, bias, act, gate, r, rs, y, ys, yh, type, Bt, L,
+                              K, N, ws, ws_bytes, status, None)
+
+
+@pytest.mark.parametrize("kw,want", [
+    (dict(x=None), b.ERR_INVALID_ARG), (dict(w=None), b.ERR_INVALID_ARG),
+    (dict(y=None), b.ERR_INVALID_ARG), (dict(x=ODD), b.ERR_INVALID_ARG),
+    (dict(w=ODD), b.ERR_INVALID_ARG),
+    (dict(y=ctypes.c_void_p((1 << 20) + 1)), b.ERR_INVALID_ARG),
+    (dict(bias=ctypes.c_void_p((1 << 20) + 1)), b.ERR_INVALID_ARG),
+    (dict(Bt=0), b.ERR_INVALID_ARG), (dict(L=0), b.ERR_INVALID_ARG),
+    (dict(K=0), b.ERR_INVALID_ARG), (dict(N=0), b.ERR_INVALID_ARG),
+    (dict(xh=0), b.ERR_INVALID_ARG), (dict(yh=-1), b.ERR_INVALID_ARG),
+    (dict(xh=3), b.ERR_INVALID_ARG), (dict(yh=5), b.ERR_INVALID_ARG),
+    (dict(xh=4), b.ERR_UNSUPPORTED), (dict(yh=2), b.ERR_UNSUPPORTED),
+    (dict(act=-1), b.ERR_INVALID_ARG), (dict(act=4), b.ERR_INVALID_ARG),
+    (dict(type=2), b.ERR_UNSUPPORTED), (dict(type=3), b.ERR_INVALID_ARG),
+    (dict(w_row=64), b.ERR_INVALID_ARG), (dict(w_row=-128), b.ERR_INVALID_ARG),
+    (dict(w_row=132), b.ERR_UNSUPPORTED), (dict(K=124), b.ERR_UNSUPPORTED),
+    (dict(xs=b.Strides(1024, 0, 0)), b.ERR_INVALID_ARG),
+    (dict(xs=b.Strides(1024, 0, 132)), b.ERR_UNSUPPORTED),
+    (dict(xs=b.Strides(-1024, 0, 128)), b.ERR_INVALID_ARG),
+    (dict(ys=b.Strides(0, 0, 192)), b.ERR_INVALID_ARG),
+    (dict(ys=b.Strides(1536, 0, 0)), b.ERR_INVALID_ARG),
+    (dict(r=P, rs=b.Strides(1536, 0, -192)), b.ERR_INVALID_ARG),
+    (dict(Bt=2 ** 15, L=2 ** 15), b.ERR_UNSUPPORTED),
+    (dict(Bt=2 ** 14, L=2 ** 15, N=2 ** 20), b.ERR_UNSUPPORTED)])
+def test_linear_refuses(kw, want):
+    assert _linear(**kw) == want
