@@ -373,6 +373,40 @@ BSA_API bsa_status bsa_linear(const void* X, const bsa_strides* xs, int32_t x_he
                               int32_t L, int32_t K, int32_t N, void* workspace,
                               size_t ws_bytes, int32_t* status, void* stream);
 
+/* Bytes of device workspace bsa_cross_forward needs; 0 if none. */
+BSA_API size_t bsa_cross_workspace_bytes(int32_t Bt, int32_t H, int32_t Hkv, int32_t Lq,
+                                         int32_t Lk, int32_t d);
+
+/* bsa_cross_forward — attention of the image or video tokens over an encoder's states, whose
+ * length is another.
+ *     o_t = sum_n e^{s q_t.k_n} v_n / sum_n e^{s q_t.k_n}  over the real keys n
+ *   Q        `type` [Bt, H, Lq, d], strides qs;   O  the same shape, strides os (written);
+ *   K, V     `type` [Bt, Hkv, Lk, d], strides ks, vs. H is a multiple of Hkv; query head h
+ *            reads key head h / (H / Hkv). Lk may be 0 (K, V may then be NULL). In Q, K and V
+ *            a batch or head stride of 0 repeats one tensor;
+ *   type     bf16 or fp16; d 64 or 128; bases 16-byte aligned. Scores, the running maximum
+ *            and sum, and the output's sum are fp32; the weights of a tile are rounded to
+ *            `type` for the second product;
+ *   key_len  nullable device int32 [Bt]: entry b's real keys are its first key_len[b], 0..Lk
+ *            (values outside report BSA_ERR_BAD_PADDING and are clamped);
+ *   key_mask nullable device uint8 [Bt, Lk]: a key whose byte is 0 is not real. With both, a
+ *            key is real if both say so. What K and V hold where a key is not real (NaN, say)
+ *            never matters;
+ *   scale    0 selects 1/sqrt(d);
+ *   lse      nullable fp32 [Bt, H, Lq]: the natural logarithm of the denominator.
+ * A row without a real key outputs zeros and lse = -inf.
+ *   workspace  device, >= bsa_cross_workspace_bytes(...) bytes, contents scratch: with few
+ *            query rows the keys are split over the GPU and their parts joined (always in one
+ *            order: the same bits on every run);
+ *   status   see the conventions. */
+BSA_API bsa_status bsa_cross_forward(const void* Q, const bsa_strides* qs, const void* K,
+                                     const bsa_strides* ks, const void* V, const bsa_strides* vs,
+                                     int32_t type, int32_t Bt, int32_t H, int32_t Hkv, int32_t Lq,
+                                     int32_t Lk, int32_t d, const int32_t* key_len,
+                                     const uint8_t* key_mask, float scale, void* O,
+                                     const bsa_strides* os, float* lse, void* workspace,
+                                     size_t ws_bytes, int32_t* status, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -33,7 +33,8 @@ CALL_BUILD_MASK, CALL_PRECOMPUTE, CALL_ROUTE, CALL_FORWARD = 0, 1, 2, 3
 EXPORTS = ("bsa_version", "bsa_status_string", "bsa_mask_blocks", "bsa_workspace_bytes",
            "bsa_build_mask", "bsa_precompute", "bsa_route", "bsa_forward",
            "bsa_forward_noalloc", "bsa_selftest_wait_timeout", "bsa_selftest_forward_timeout",
-           "bsa_rotary", "bsa_linear_workspace_bytes", "bsa_linear")
+           "bsa_rotary", "bsa_linear_workspace_bytes", "bsa_linear",
+           "bsa_cross_workspace_bytes", "bsa_cross_forward")
 
 
 class BsaError(RuntimeError):
@@ -79,6 +80,9 @@ _SIGS = {
     "bsa_linear_workspace_bytes": (_sz, [_i32, _i32, _i32, _i32]),
     "bsa_linear": (_i32, [_vp, _sp, _i32, _vp, _i64, _vp, _i32, _vp, _vp, _sp, _vp, _sp, _i32,
                           _i32, _i32, _i32, _i32, _i32, _vp, _sz, _vp, _vp]),
+    "bsa_cross_workspace_bytes": (_sz, [_i32, _i32, _i32, _i32, _i32, _i32]),
+    "bsa_cross_forward": (_i32, [_vp, _sp, _vp, _sp, _vp, _sp, _i32, _i32, _i32, _i32, _i32, _i32,
+                                 _i32, _vp, _vp, _f32, _vp, _sp, _vp, _vp, _sz, _vp, _vp]),
 }
 
 
@@ -389,15 +393,44 @@ def bsa_linear(X, W, Y, bias=None, act=ACT_NONE, gate=None, R=None, workspace=No
     if W.stride(1) != 1 and K > 1:
         raise ValueError("W's rows must be contiguous")
     rs = None if R is None else ys if R is Y else _strided(R, "R", X, Y.shape)
-    ws_bytes = 0
-    if workspace is not None:
-        if not workspace.is_cuda or workspace.device != dev:
-            raise ValueError(f"workspace must be on {dev}")
-        ws_bytes = workspace.numel() * workspace.element_size()
+    ws, ws_bytes = _workspace_of(workspace, dev)
     _call("bsa_linear", dev, stream, X.data_ptr(), xs, x_heads, W.data_ptr(),
           W.stride(0) if N > 1 else 0, _plain(bias, dtype, "bias", (N,), dev), act,
           _plain(gate, dtype, "gate", (Bt, N), dev), None if R is None else R.data_ptr(), rs,
-          Y.data_ptr(), ys, y_heads, TYPES[dtype], Bt, L, K, N, _ptr(workspace), ws_bytes,
+          Y.data_ptr(), ys, y_heads, TYPES[dtype], Bt, L, K, N, ws, ws_bytes,
+          _status_ptr(status, dev))
+
+
+def bsa_cross_workspace_bytes(Bt: int, H: int, Hkv: int, Lq: int, Lk: int, d: int) -> int:
+    return int(lib().bsa_cross_workspace_bytes(Bt, H, Hkv, Lq, Lk, d))
+
+
+def _workspace_of(ws, device):
+    """(address, bytes) of a workspace tensor on `device`, or of none."""
+    if ws is None:
+        return None, 0
+    if not ws.is_cuda or ws.device != device:
+        raise ValueError(f"workspace must be on {device}")
+    return ws.data_ptr(), ws.numel() * ws.element_size()
+
+
+def bsa_cross_forward(Q, K, V, O, key_len=None, key_mask=None, scale=0.0, lse=None,
+                      workspace=None, status=None, stream=None):
+    qs = _strided(Q, "Q")
+    ks = _strided(K, "K", Q)
+    vs = _strided(V, "V", Q, K.shape)
+    os_ = _strided(O, "O", Q, Q.shape)
+    Bt, H, Lq, d = Q.shape
+    Hkv, Lk = K.shape[1], K.shape[2]
+    if K.shape[0] != Bt or K.shape[3] != d:
+        raise ValueError(f"K has shape {tuple(K.shape)}, Q {tuple(Q.shape)}")
+    dev = Q.device
+    ws, ws_bytes = _workspace_of(workspace, dev)
+    _call("bsa_cross_forward", dev, stream, Q.data_ptr(), qs, K.data_ptr(), ks, V.data_ptr(), vs,
+          TYPES[Q.dtype], Bt, H, Hkv, Lq, Lk, d,
+          _plain(key_len, torch.int32, "key_len", (Bt,), dev),
+          _plain(key_mask, torch.uint8, "key_mask", (Bt, Lk), dev), scale, O.data_ptr(), os_,
+          _plain(lse, torch.float32, "lse", (Bt, H, Lq), dev), ws, ws_bytes,
           _status_ptr(status, dev))
 
 
@@ -487,6 +520,22 @@ def linear(X, W, bias=None, act=ACT_NONE, gate=None, residual=None, heads=0, sta
             ws = torch.empty(need, dtype=torch.uint8, device=X.device)
     bsa_linear(X, W, out, bias, act, gate, residual, ws, status, stream)
     return out
+
+
+def cross_forward(Q, K, V, key_len=None, key_mask=None, scale=0.0, want_lse=False, status=None,
+                  ws=None, out=None, stream=None):
+    """Attention of Q [Bt, H, Lq, d] over K, V [Bt, Hkv, Lk, d] (any strides; H a multiple of
+    Hkv): the first key_len[b] (int32 [Bt]) keys of each entry, those whose key_mask (uint8
+    [Bt, Lk]) is not 0, or all. Returns (O contiguous or `out`, lse fp32 [Bt, H, Lq] or None)."""
+    O = Q.new_empty(Q.shape) if out is None else out
+    lse = Q.new_empty(Q.shape[:3], dtype=torch.float32) if want_lse else None
+    if ws is None:
+        need = bsa_cross_workspace_bytes(*Q.shape[:2], K.shape[1], Q.shape[2], K.shape[2],
+                                         Q.shape[3])
+        if need:
+            ws = torch.empty(need, dtype=torch.uint8, device=Q.device)
+    bsa_cross_forward(Q, K, V, O, key_len, key_mask, scale, lse, ws, status, stream)
+    return O, lse
 
 
 def default_scale(d: int) -> float:

@@ -63,6 +63,17 @@ bsa_status check_strides(const bsa_strides& s, int elem_bytes) {
   return BSA_OK;
 }
 
+bsa_status check_cross(int Bt, int H, int Hkv, int Lq, int Lk, int d) {
+  if (Bt <= 0 || H <= 0 || Hkv <= 0 || Lq <= 0 || Lk < 0) return BSA_ERR_INVALID_ARG;
+  if (H % Hkv != 0) return BSA_ERR_INVALID_ARG;
+  if (d != 64 && d != 128) return BSA_ERR_UNSUPPORTED;
+  // rows, keys and work items are counted in 32 bits, with room for tiles past the end
+  if ((int64_t)Bt * H >= (int64_t)1 << 24 || Lq >= 1 << 30 || Lk >= 1 << 30 ||
+      (int64_t)Bt * H * (((int64_t)Lq + 255) / 256) >= (int64_t)1 << 22)
+    return BSA_ERR_UNSUPPORTED;
+  return BSA_OK;
+}
+
 }  // namespace
 
 namespace bsa {
@@ -304,6 +315,47 @@ bsa_status bsa_linear(const void* X, const bsa_strides* xs, int32_t x_heads, con
   if (!workspace_ok(bsa::linear_workspace(Bt, L, K, N), workspace, ws_bytes))
     return BSA_ERR_WORKSPACE;
   return from_cuda(bsa::launch_linear(a, static_cast<cudaStream_t>(stream)));
+}
+
+size_t bsa_cross_workspace_bytes(int32_t Bt, int32_t H, int32_t Hkv, int32_t Lq, int32_t Lk,
+                                 int32_t d) {
+  if (check_cross(Bt, H, Hkv, Lq, Lk, d) != BSA_OK) return 0;
+  return bsa::cross_workspace(Bt, H, Lq, Lk, d);
+}
+
+bsa_status bsa_cross_forward(const void* Q, const bsa_strides* qs, const void* K,
+                             const bsa_strides* ks, const void* V, const bsa_strides* vs,
+                             int32_t type, int32_t Bt, int32_t H, int32_t Hkv, int32_t Lq,
+                             int32_t Lk, int32_t d, const int32_t* key_len,
+                             const uint8_t* key_mask, float scale, void* O, const bsa_strides* os,
+                             float* lse, void* workspace, size_t ws_bytes, int32_t* status,
+                             void* stream) {
+  bsa_status r = check_cross(Bt, H, Hkv, Lq, Lk, d);
+  if (r != BSA_OK) return r;
+  if (!Q || !O || (Lk > 0 && (!K || !V))) return BSA_ERR_INVALID_ARG;
+  if (type != BSA_TYPE_BF16 && type != BSA_TYPE_FP16)
+    return type == BSA_TYPE_FP32 ? BSA_ERR_UNSUPPORTED : BSA_ERR_INVALID_ARG;
+  if (!aligned16(Q) || !aligned16(K) || !aligned16(V) || !aligned16(O)) return BSA_ERR_INVALID_ARG;
+  if ((reinterpret_cast<uintptr_t>(key_len) & 3u) != 0 ||
+      (reinterpret_cast<uintptr_t>(lse) & 3u) != 0)
+    return BSA_ERR_INVALID_ARG;
+  if (!(scale >= 0.f) || !(scale <= 1e30f)) return BSA_ERR_INVALID_ARG;
+  bsa::CrossArgs a{Q, strides_of(qs, Bt, H, Lq, d), K, strides_of(ks, Bt, Hkv, Lk, d), V,
+                   strides_of(vs, Bt, Hkv, Lk, d), type, Bt, H, Hkv, Lq, Lk, d, key_len, key_mask,
+                   bsa::forward_scale(scale, d), O, strides_of(os, Bt, H, Lq, d), lse, workspace,
+                   status};
+  for (const bsa_strides& s : {a.qs, a.ks, a.vs, a.os}) {
+    r = check_strides(s, 2);
+    if (r != BSA_OK) return r;
+    if (s.batch >= (int64_t)1 << 39 || s.head >= (int64_t)1 << 39 || s.row >= (int64_t)1 << 39)
+      return BSA_ERR_UNSUPPORTED;  // a tensor map's stride is below 2^40 bytes
+  }
+  if ((Lq > 1 && (a.qs.row == 0 || a.os.row == 0)) || (Lk > 1 && (a.ks.row == 0 || a.vs.row == 0)))
+    return BSA_ERR_INVALID_ARG;
+  if ((Bt > 1 && a.os.batch == 0) || (H > 1 && a.os.head == 0)) return BSA_ERR_INVALID_ARG;
+  if (!workspace_ok(bsa::cross_workspace(Bt, H, Lq, Lk, d), workspace, ws_bytes))
+    return BSA_ERR_WORKSPACE;
+  return from_cuda(bsa::launch_cross(a, static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

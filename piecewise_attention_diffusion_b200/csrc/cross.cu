@@ -1,0 +1,696 @@
+// bsa_cross_forward: attention of Lq queries over Lk keys of another sequence (an encoder's
+// states) on the 5th-generation tensor cores (tcgen05 + TMEM + TMA), sm_100a.
+//
+//     o_t = sum_n p_tn v_n / l_t,  p_tn = e^{s q_t.k_n - m_t},  l_t = sum_n p_tn
+// over the real keys n of the batch entry (the first key_len of them, and those whose
+// key_mask byte is not 0), in one pass over the keys with a running maximum m and sum l per
+// row, both fp32.
+//
+// k_cross: one persistent CTA per SM, 384 threads. A work item is 256 query rows of one head
+// (and one run of key tiles, where the keys are split); its two tiles of 128 rows
+// ("streams") share every K and V tile, and the softmax of one overlaps the tensor-core work
+// of the other:
+//   warps 0-3, 4-7  one softmax warpgroup per stream: thread r owns query row r (TMEM lane
+//           r): scores to registers, row maximum, P = 2^(x - m) back to TMEM in 16 bits, O
+//           rescaled only when the maximum grows by more than 2^8; then the epilogue;
+//   warp 8  TMA producer of a ring of K and V tiles of 128 keys;
+//   warp 9  MMA issuer: S(t) = Q K(t)^T, O += P(t) V(t) with P as the TMEM operand;
+//   warp 10 clears the rows of V that the mask excludes, so that what lies there (infinities,
+//           NaN) meets no product: P is 0 there, but 0 * inf is not;
+//   warp 11 idle (it completes the warpgroup that gives its registers up).
+// TMEM: S0 [0,128), S1 [128,256), O0 [256, 256 + D), O1 [256 + D, 256 + 2 D); P overlays S.
+// Few rows: the keys are split into runs that separate items take; each leaves its O, m and l
+// in the workspace, and k_join adds them in order.
+// Every mbarrier wait is bounded; on a timeout the CTA drains, frees TMEM and reports
+// BSA_ERR_TIMEOUT.
+#include <algorithm>
+
+#include "common.cuh"
+#include "forward_tiles.cuh"
+#include "internal.h"
+#include "sm100.cuh"
+#include "types.cuh"
+
+namespace bsa {
+namespace cross {
+
+using namespace sm100;
+
+constexpr int kBQ = 128;  // query rows per stream
+constexpr int kBK = 128;  // keys per tile
+constexpr int kStreams = 2;
+constexpr int kThreads = 384;
+constexpr int kProducerWarp = 8, kMmaWarp = 9, kClearWarp = 10;
+// register split as in the block attention: 128 x 88 + 256 x 208 = 384 x 168
+constexpr int kRegsControl = 88, kRegsSoftmax = 208;
+static_assert(128 * kRegsControl + 256 * kRegsSoftmax <= kThreads * 168, "register split");
+constexpr float kRescaleLog2 = 8.0f;
+
+struct Params {
+  int Bt, H, share, Lq, Lk;  // share: query heads per key head
+  int q_tiles;               // of 256 rows
+  int splits, tiles_per_split;
+  int n_items;
+  int qb, qh, kb, kh, vb, vh;  // 0 where that stride is 0 (one copy for all)
+  const int32_t* key_len;
+  const uint8_t* key_mask;
+  float scale_log2;
+  float* lse;
+  float* part_o;   // [splits, Bt H Lq, D]
+  float2* part_ml; // [splits, Bt H Lq]: running maximum (base 2) and sum
+  int32_t* status;
+  uint64_t wait_ns;
+};
+
+template <int D>
+struct Cfg {
+  static constexpr int QBYTES = kBQ * D * 2;
+  static constexpr int SLOT = kBK * D * 2;
+  static constexpr int NK = D == 128 ? 2 : 4;  // slots of the K ring
+  static constexpr int NV = D == 128 ? 3 : 4;  // and of the V ring
+  static constexpr int SMEM = kStreams * QBYTES + (NK + NV) * SLOT + 1024;
+  __host__ __device__ static constexpr uint32_t S_COL(int x) { return 128u * x; }
+  __host__ __device__ static constexpr uint32_t O_COL(int x) { return 256u + D * x; }
+};
+
+struct Item {
+  int b, h, qt, split, len, t0, n;  // n key tiles from tile t0
+  bool two;                         // the second stream has rows
+};
+
+__device__ __forceinline__ Item item_of(const Params& p, int i) {
+  Item r;
+  r.split = i % p.splits;
+  i /= p.splits;
+  r.qt = i % p.q_tiles;
+  i /= p.q_tiles;
+  r.h = i % p.H;
+  r.b = i / p.H;
+  r.len = p.key_len != nullptr ? min(max(__ldg(p.key_len + r.b), 0), p.Lk) : p.Lk;
+  r.t0 = r.split * p.tiles_per_split;
+  r.n = min(max(ceil_div(r.len, kBK) - r.t0, 0), p.tiles_per_split);
+  r.two = r.qt * 2 * kBQ + kBQ < p.Lq;
+  return r;
+}
+
+// Whether tile t of an item has keys that are not real.
+__device__ __forceinline__ bool tile_masked(const Params& p, const Item& it, int t) {
+  return p.key_mask != nullptr || (it.t0 + t + 1) * kBK > it.len;
+}
+
+// The tile's excluded keys as 128 bits, the same in every lane of the warp.
+__device__ __forceinline__ void excluded(const Params& p, const Item& it, int t, int lane,
+                                         uint32_t (&w)[4]) {
+  const int key0 = (it.t0 + t) * kBK;
+  uint32_t own = 0;  // keys 4 lane .. 4 lane + 3
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int key = key0 + 4 * lane + i;
+    bool out = key >= it.len;
+    if (!out && p.key_mask != nullptr) out = __ldg(p.key_mask + (int64_t)it.b * p.Lk + key) == 0;
+    own |= (out ? 1u : 0u) << i;
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    w[i] = __reduce_or_sync(0xffffffffu, lane / 8 == i ? own << (lane % 8 * 4) : 0u);
+}
+
+struct Barriers {
+  uint64_t k_full[4], k_empty[4], v_full[4], v_empty[4], v_clear[4];
+  uint64_t q_full[kStreams];
+  uint64_t s_full[kStreams], p_full[kStreams];
+  uint64_t o_final[kStreams], o_free[kStreams], o_staged[kStreams];
+  uint64_t done;
+};
+
+template <typename T>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  if (is_bf16<T>()) return pack_bf16x2(lo, hi);
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// P of one row: 2^(s * scale_log2 - m_ref), to TMEM in pairs of T at p_addr; returns the fp32
+// sum.
+template <typename T>
+__device__ __forceinline__ float row_exp(const uint32_t (&r)[kBK], float scale_log2, float m_ref,
+                                         uint32_t p_addr) {
+  const float2 sc = make_float2(scale_log2, scale_log2), nm = make_float2(-m_ref, -m_ref);
+  float2 acc[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f),
+                   make_float2(0.f, 0.f)};
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    uint32_t pk[32];
+#pragma unroll
+    for (int q = 0; q < 32; ++q) {
+      const int e = h * 64 + 2 * q;
+      const float2 x = fma2(make_float2(__uint_as_float(r[e]), __uint_as_float(r[e + 1])), sc, nm);
+      const float2 v = make_float2(ex2(x.x), ex2(x.y));
+      acc[q & 3] = add2(acc[q & 3], v);
+      pk[q] = pack2<T>(v.x, v.y);
+    }
+    tmem_st32(p_addr + h * 32, pk);
+  }
+  const float2 a = add2(add2(acc[0], acc[1]), add2(acc[2], acc[3]));
+  return a.x + a.y;
+}
+
+__device__ __forceinline__ void tma_load_5d(void* dst, const CUtensorMap* map, uint64_t* bar, int x,
+                                            int y, int z, int w, int v) {
+  asm volatile(
+      "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+      "[%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(v),
+      "r"(smem_u32(bar))
+      : "memory");
+}
+
+__device__ __forceinline__ void tma_store_5d(const CUtensorMap* map, const void* src, int x, int y,
+                                             int z, int w, int v) {
+  asm volatile(
+      "cp.async.bulk.tensor.5d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4, %5, %6}], [%1];"
+      ::"l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(src)), "r"(x), "r"(y), "r"(z), "r"(w),
+      "r"(v)
+      : "memory");
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kThreads, 1)
+k_cross(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+        const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmO,
+        const __grid_constant__ Params p) {
+  using C = Cfg<D>;
+  extern __shared__ unsigned char smem_raw[];
+  unsigned char* smem = reinterpret_cast<unsigned char*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  unsigned char* sK = smem + kStreams * C::QBYTES;
+  unsigned char* sV = sK + C::NK * C::SLOT;
+  __shared__ Barriers bars;
+  __shared__ uint32_t tmem_base_sh;
+  __shared__ int abort_sh;
+
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  if (threadIdx.x == 0) {
+    abort_sh = 0;
+    for (int x = 0; x < kStreams; ++x) {
+      mbar_init(&bars.q_full[x], 1);
+      mbar_init(&bars.s_full[x], 1);
+      mbar_init(&bars.p_full[x], 128);
+      mbar_init(&bars.o_final[x], 1);
+      mbar_init(&bars.o_free[x], 128);
+      mbar_init(&bars.o_staged[x], 128);
+    }
+    for (int i = 0; i < C::NK; ++i) {
+      mbar_init(&bars.k_full[i], 1);
+      mbar_init(&bars.k_empty[i], 1);
+    }
+    for (int i = 0; i < C::NV; ++i) {
+      mbar_init(&bars.v_full[i], 1);
+      mbar_init(&bars.v_empty[i], 1);
+      mbar_init(&bars.v_clear[i], 32);
+    }
+    mbar_init(&bars.done, 1);
+    fence_barrier_init();
+  }
+  if (warp == kMmaWarp) {
+    tmem_alloc(&tmem_base_sh, 512);
+    tmem_relinquish();
+  }
+  if (warp == kProducerWarp && lane == 0) {
+    prefetch_tensormap(&tmQ);
+    prefetch_tensormap(&tmK);
+    prefetch_tensormap(&tmV);
+    prefetch_tensormap(&tmO);
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tmem_base_sh;
+  volatile int* abort_flag = &abort_sh;
+  const bool clearing = p.key_len != nullptr || p.key_mask != nullptr;
+
+  if (warp >= kProducerWarp) {
+    setmaxnreg_dec<kRegsControl>();
+    if (warp == kProducerWarp) {
+      // ------------------------------------------------ TMA producer: K0, V0, K1, V1, ...
+      if (lane == 0) {
+        uint32_t nk = 0, nv = 0;  // tiles loaded so far
+        bool ok = true;
+        for (int i = blockIdx.x; i < p.n_items && ok; i += gridDim.x) {
+          const Item it = item_of(p, i);
+          const int hk = it.h / p.share;
+          for (int t = 0; t < it.n && ok; ++t) {
+            const int row = (it.t0 + t) * kBK;
+            const int ks = nk % C::NK, vs = nv % C::NV;
+            ok = mbar_wait(&bars.k_empty[ks], ((nk / C::NK) & 1) ^ 1, abort_flag, p.wait_ns);
+            if (!ok) break;
+            mbar_arrive_expect_tx(&bars.k_full[ks], C::SLOT);
+            tma_load_5d(sK + ks * C::SLOT, &tmK, &bars.k_full[ks], 0, row, 0, hk * p.kh, it.b * p.kb);
+            ++nk;
+            ok = mbar_wait(&bars.v_empty[vs], ((nv / C::NV) & 1) ^ 1, abort_flag, p.wait_ns);
+            if (!ok) break;
+            mbar_arrive_expect_tx(&bars.v_full[vs], C::SLOT);
+            tma_load_5d(sV + vs * C::SLOT, &tmV, &bars.v_full[vs], 0, row, 0, hk * p.vh, it.b * p.vb);
+            ++nv;
+          }
+        }
+        if (!ok) {
+          // drain: wait (bounded, ignoring the abort flag) for copies still in flight
+          const uint64_t t0 = globaltimer_ns();
+          for (uint32_t r = nk > (uint32_t)C::NK ? nk - C::NK : 0; r < nk; ++r)
+            while (!mbar_try_wait(&bars.k_full[r % C::NK], (r / C::NK) & 1) &&
+                   globaltimer_ns() - t0 < 100000000ull) {
+            }
+          for (uint32_t r = nv > (uint32_t)C::NV ? nv - C::NV : 0; r < nv; ++r)
+            while (!mbar_try_wait(&bars.v_full[r % C::NV], (r / C::NV) & 1) &&
+                   globaltimer_ns() - t0 < 100000000ull) {
+            }
+        }
+      }
+      __syncwarp();
+    } else if (warp == kMmaWarp) {
+      // -------------------------------------------------------------------- MMA issuer
+      if (lane == 0) {
+        constexpr uint32_t fmt = is_bf16<T>() ? 1u : 0u;
+        constexpr uint32_t ab = (1u << 4) | (fmt << 7) | (fmt << 10) | ((uint32_t)(kBQ >> 4) << 24);
+        constexpr uint32_t idesc_s = ab | ((uint32_t)(kBK >> 3) << 17);
+        constexpr uint32_t idesc_o = ab | (1u << 16) | ((uint32_t)(D >> 3) << 17);  // V is MN-major
+        uint32_t nk = 0, nv = 0;  // tiles taken so far
+        int items[kStreams] = {0, 0};
+        uint32_t p_count[kStreams] = {0, 0};
+        bool ok = true;
+        auto issue_s = [&](int x, uint32_t k_addr) {
+          const uint64_t a0 = smem_desc_sw128(smem_u32(smem + x * C::QBYTES), 16, 1024);
+          const uint64_t b0 = smem_desc_sw128(k_addr, 16, 1024);
+#pragma unroll
+          for (int k = 0; k < D / 16; ++k) {
+            const uint64_t off = (uint64_t)(((k / 4) * (kBQ * 128) + (k % 4) * 32) >> 4);
+            mma_ss(tmem + C::S_COL(x), a0 + off, b0 + off, idesc_s, k > 0 ? 1u : 0u);
+          }
+          mma_commit(&bars.s_full[x]);
+        };
+        for (int i = blockIdx.x; i < p.n_items && ok; i += gridDim.x) {
+          const Item it = item_of(p, i);
+          const int ns = it.two ? 2 : 1;
+          if (it.n > 0)
+            ok = mbar_wait(&bars.k_full[nk % C::NK], (nk / C::NK) & 1, abort_flag, p.wait_ns);
+          for (int x = 0; x < ns && ok; ++x) {
+            // this item's Q is loaded, and the stream's last epilogue has read S and O
+            ok = mbar_wait(&bars.q_full[x], items[x] & 1, abort_flag, p.wait_ns) &&
+                 (items[x] == 0 ||
+                  mbar_wait(&bars.o_free[x], (items[x] - 1) & 1, abort_flag, p.wait_ns));
+            if (!ok) break;
+            tc_fence_after();
+            if (it.n > 0) issue_s(x, smem_u32(sK + nk % C::NK * C::SLOT));
+            ++items[x];
+          }
+          if (!ok) break;
+          if (it.n > 0) mma_commit(&bars.k_empty[nk++ % C::NK]);
+          for (int t = 0; t < it.n && ok; ++t) {
+            const bool more = t + 1 < it.n;
+            const uint32_t vs = nv % C::NV, ks = nk % C::NK;
+            // V(t), cleared of what is masked where there are masks, and K(t + 1)
+            ok = mbar_wait(&bars.v_full[vs], (nv / C::NV) & 1, abort_flag, p.wait_ns) &&
+                 (!clearing || mbar_wait(&bars.v_clear[vs], (nv / C::NV) & 1, abort_flag, p.wait_ns)) &&
+                 (!more || mbar_wait(&bars.k_full[ks], (nk / C::NK) & 1, abort_flag, p.wait_ns));
+            for (int x = 0; x < ns && ok; ++x) {
+              ok = mbar_wait(&bars.p_full[x], p_count[x] & 1, abort_flag, p.wait_ns);
+              if (!ok) break;
+              ++p_count[x];
+              tc_fence_after();
+              const uint64_t b0 = smem_desc_sw128(smem_u32(sV + vs * C::SLOT), kBK * 128, 1024);
+#pragma unroll
+              for (int k = 0; k < kBK / 16; ++k)
+                mma_ts(tmem + C::O_COL(x), tmem + C::S_COL(x) + k * 8, b0 + (uint64_t)(k * 128),
+                       idesc_o, (t | k) ? 1u : 0u);
+              if (more) issue_s(x, smem_u32(sK + ks * C::SLOT));
+            }
+            if (!ok) break;
+            mma_commit(&bars.v_empty[vs]);
+            ++nv;
+            if (more) {
+              mma_commit(&bars.k_empty[ks]);
+              ++nk;
+            }
+          }
+          if (!ok) break;
+          for (int x = 0; x < ns; ++x) mma_commit(&bars.o_final[x]);
+        }
+        // every issued MMA must complete before TMEM is released
+        mma_commit(&bars.done);
+        const uint64_t t0 = globaltimer_ns();
+        while (!mbar_try_wait(&bars.done, 0) && globaltimer_ns() - t0 < 100000000ull) {
+        }
+      }
+      __syncwarp();
+    } else if (warp == kClearWarp) {
+      // ------------------------------------------------- rows of V that are not real keys
+      // Every V tile passes here, masked or not, so that this warp and the ring's barrier are
+      // never more than one phase apart.
+      uint32_t nv = 0;
+      bool ok = clearing;
+      for (int i = blockIdx.x; i < p.n_items && ok; i += gridDim.x) {
+        const Item it = item_of(p, i);
+        if (p.key_len != nullptr && lane == 0) {
+          const int n = __ldg(p.key_len + it.b);
+          if (n < 0 || n > p.Lk) report(p.status, BSA_ERR_BAD_PADDING);
+        }
+        for (int t = 0; t < it.n && ok; ++t, ++nv) {
+          const bool masked = tile_masked(p, it, t);
+          uint32_t w[4];
+          if (masked) excluded(p, it, t, lane, w);
+          const int slot = nv % C::NV;
+          ok = mbar_wait(&bars.v_full[slot], (nv / C::NV) & 1, abort_flag, p.wait_ns);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          if (masked) {
+            // row k: 128 bytes in each of the D / 64 sub-tiles; a lane clears 16 of them
+            constexpr int kPieces = D / 8;
+            const int piece = lane % kPieces;
+            unsigned char* v = sV + slot * C::SLOT + (piece / 8) * (kBK * 128) + (piece % 8) * 16;
+            for (int k = lane / kPieces; k < kBK; k += 32 / kPieces) {
+              const uint32_t word = k < 64 ? (k < 32 ? w[0] : w[1]) : (k < 96 ? w[2] : w[3]);
+              if ((word >> (k & 31)) & 1u)
+                *reinterpret_cast<uint4*>(v + k * 128) = make_uint4(0u, 0u, 0u, 0u);
+            }
+            fence_proxy_async_smem();
+          }
+          mbar_arrive(&bars.v_clear[slot]);
+        }
+      }
+    }
+  } else {
+    setmaxnreg_inc<kRegsSoftmax>();
+    // ------------------------------------------------------- softmax + epilogue (per stream)
+    // P in fp16 is kept 2^7 times larger (at most 2^15, after the lazy rescale's 2^8), so that
+    // keys up to 2^-31 below the row's largest still count
+    constexpr float kLift = is_bf16<T>() ? 0.f : 7.f;
+    const int x = warp / 4, quad = warp % 4, row = quad * 32 + lane;
+    const bool leader = quad == 0 && lane == 0;
+    const uint32_t lane_addr = (uint32_t)(quad * 32) << 16;
+    const uint32_t s_base = tmem + lane_addr + C::S_COL(x);
+    const uint32_t o_base = tmem + lane_addr + C::O_COL(x);
+    unsigned char* sq = smem + x * C::QBYTES;
+    // the next item from `from` on that has rows for this stream
+    auto next_item = [&](int from) -> int {
+      for (int i = from; i < p.n_items; i += gridDim.x)
+        if (x == 0 || (i / p.splits % p.q_tiles) * 2 * kBQ + kBQ < p.Lq) return i;
+      return p.n_items;
+    };
+    auto load_q = [&](int i) {
+      const Item it = item_of(p, i);
+      mbar_arrive_expect_tx(&bars.q_full[x], C::QBYTES);
+      tma_load_5d(sq, &tmQ, &bars.q_full[x], 0, it.qt * 2 * kBQ + x * kBQ, 0, it.h * p.qh, it.b * p.qb);
+    };
+    int q_issued = 0;
+    int i = next_item(blockIdx.x);
+    if (leader && i < p.n_items) {
+      load_q(i);
+      ++q_issued;
+    }
+    uint32_t tiles = 0;
+    bool ok = true;
+    for (int k = 0; i < p.n_items && ok; ++k) {
+      const Item it = item_of(p, i);
+      const int following = next_item(i + gridDim.x);
+      const int row_g = it.qt * 2 * kBQ + x * kBQ + row;
+      float m_run = -INFINITY, l = 0.f;
+      for (int t = 0; t < it.n; ++t) {
+        const bool masked = tile_masked(p, it, t);
+        uint32_t excl[4] = {0u, 0u, 0u, 0u};
+        if (masked) excluded(p, it, t, lane, excl);
+        ok = mbar_wait(&bars.s_full[x], tiles & 1, abort_flag, p.wait_ns);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        ++tiles;
+        tc_fence_after();
+        uint32_t r[kBK];
+        tmem_ld32(s_base, *reinterpret_cast<uint32_t(*)[32]>(r));
+        tmem_ld32(s_base + 32, *reinterpret_cast<uint32_t(*)[32]>(r + 32));
+        tmem_ld32(s_base + 64, *reinterpret_cast<uint32_t(*)[32]>(r + 64));
+        tmem_ld32(s_base + 96, *reinterpret_cast<uint32_t(*)[32]>(r + 96));
+        tmem_wait_ld();
+        if (masked) {
+#pragma unroll
+          for (int e = 0; e < kBK; ++e)
+            if ((excl[e >> 5] >> (e & 31)) & 1u) r[e] = __float_as_uint(-INFINITY);
+        }
+        const float mx = fwdtiles::row_max<kBK, kBK>(r) * p.scale_log2;
+        const bool need = mx > m_run + kRescaleLog2;
+        if (__any_sync(0xffffffffu, need)) {
+          const float m_new = need ? mx : m_run;
+          const float factor = need ? ex2(m_run - m_new) : 1.0f;
+          if (t > 0) {
+            // PV(t-1) was issued before S(t), so it has completed: rescale O in TMEM
+#pragma unroll 1
+            for (int c = 0; c < D; c += 16) {
+              uint32_t ro[16];
+              tmem_ld16(o_base + c, ro);
+              tmem_wait_ld();
+#pragma unroll
+              for (int e = 0; e < 16; ++e) ro[e] = __float_as_uint(__uint_as_float(ro[e]) * factor);
+              tmem_st16(o_base + c, ro);
+            }
+          }
+          l *= factor;
+          m_run = m_new;
+        }
+        const float m_ref = m_run == -INFINITY ? 0.f : m_run - kLift;
+        l += row_exp<T>(r, p.scale_log2, m_ref, s_base);
+        tmem_wait_st();
+        tc_fence_before();
+        mbar_arrive(&bars.p_full[x]);
+      }
+      if (!ok) break;
+
+      // ------------------------------------------------------------------ epilogue
+      ok = mbar_wait(&bars.o_final[x], k & 1, abort_flag, p.wait_ns);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      tc_fence_after();
+      const bool write = row_g < p.Lq;
+      const int64_t row_of = ((int64_t)it.b * p.H + it.h) * p.Lq + row_g;
+      // a row without a real key has l = 0 and outputs zeros; NaN stays NaN
+      const float inv_l = l == 0.f ? 0.f : 1.0f / l;
+      if (p.splits > 1) {
+        const int64_t at = (int64_t)it.split * p.Bt * p.H * p.Lq + row_of;
+        if (write) p.part_ml[at] = make_float2(m_run - kLift, l);
+#pragma unroll 1
+        for (int c = 0; c < D && it.n > 0; c += 16) {
+          uint32_t ro[16];
+          tmem_ld16(o_base + c, ro);
+          tmem_wait_ld();
+          if (write) {
+            uint4* dst = reinterpret_cast<uint4*>(p.part_o + at * D + c);
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              dst[e] = make_uint4(ro[4 * e], ro[4 * e + 1], ro[4 * e + 2], ro[4 * e + 3]);
+          }
+        }
+        if (leader && following < p.n_items) {
+          load_q(following);
+          ++q_issued;
+        }
+      } else {
+#pragma unroll 1
+        for (int c = 0; c < D; c += 16) {
+          uint32_t ro[16];
+          if (it.n > 0) {
+            tmem_ld16(o_base + c, ro);
+            tmem_wait_ld();
+          }
+          uint32_t packed[8];
+#pragma unroll
+          for (int e = 0; e < 16; e += 2)
+            packed[e / 2] = it.n > 0 ? pack2<T>(__uint_as_float(ro[e]) * inv_l,
+                                                __uint_as_float(ro[e + 1]) * inv_l)
+                                     : 0u;
+          // Q's tile is free: it stages the output in the same 128-byte swizzle
+          const int j = (c % 64) / 8;
+          unsigned char* dst = sq + (c / 64) * (kBQ * 128) + row * 128;
+          *reinterpret_cast<uint4*>(dst + ((j ^ (row & 7)) * 16)) =
+              make_uint4(packed[0], packed[1], packed[2], packed[3]);
+          *reinterpret_cast<uint4*>(dst + (((j + 1) ^ (row & 7)) * 16)) =
+              make_uint4(packed[4], packed[5], packed[6], packed[7]);
+        }
+        fence_proxy_async_smem();
+        mbar_arrive(&bars.o_staged[x]);
+        bool staged = true;
+        if (leader) {
+          staged = mbar_wait(&bars.o_staged[x], k & 1, abort_flag, p.wait_ns);
+          if (staged) {
+            tma_store_5d(&tmO, sq, 0, it.qt * 2 * kBQ + x * kBQ, 0, it.h, it.b);
+            bulk_commit_group();
+            bulk_wait_read_all();
+            if (following < p.n_items) {
+              load_q(following);
+              ++q_issued;
+            }
+          }
+        }
+        ok = __all_sync(0xffffffffu, staged);
+        if (!ok) break;
+        if (write && p.lse != nullptr)
+          p.lse[row_of] = l == 0.f ? -INFINITY : (m_run - kLift + log2f(l)) * 0.69314718055994531f;
+      }
+      tc_fence_before();
+      mbar_arrive(&bars.o_free[x]);
+      i = following;
+    }
+    if (leader) bulk_wait_all();
+    if (!ok && leader && q_issued > 0) {
+      // drain this stream's last Q copy (bounded) before the CTA exits
+      const uint64_t t0 = globaltimer_ns();
+      while (!mbar_try_wait(&bars.q_full[x], (q_issued - 1) & 1) &&
+             globaltimer_ns() - t0 < 100000000ull) {
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (threadIdx.x == 0 && abort_sh) report(p.status, BSA_ERR_TIMEOUT);
+  if (warp == kMmaWarp) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// The runs of one row, joined in order: m = max m_i, o = sum 2^(m_i - m) o_i / l with
+// l = sum 2^(m_i - m) l_i. One warp per row.
+template <typename T, int D>
+__global__ void __launch_bounds__(128)
+k_join(const Params p, T* o, bsa_strides os) {
+  const int64_t rows = (int64_t)p.Bt * p.H * p.Lq;
+  const int64_t row = (int64_t)blockIdx.x * 4 + threadIdx.x / 32;
+  const int lane = threadIdx.x % 32;
+  if (row >= rows) return;
+  float m = -INFINITY;
+  for (int s = 0; s < p.splits; ++s) {
+    const float2 ml = p.part_ml[s * rows + row];
+    if (ml.y != 0.f) m = fmaxf(m, ml.x);
+  }
+  constexpr int V = D / 32;
+  float acc[V] = {}, l = 0.f;
+  for (int s = 0; s < p.splits; ++s) {
+    const float2 ml = p.part_ml[s * rows + row];
+    if (ml.y == 0.f) continue;  // no real key in this run: its O was not written
+    const float w = exp2f(ml.x - m);
+    l += w * ml.y;
+    const Pack<float, V> part =
+        *reinterpret_cast<const Pack<float, V>*>(p.part_o + (s * rows + row) * D + lane * V);
+#pragma unroll
+    for (int e = 0; e < V; ++e) acc[e] += w * part.v[e];
+  }
+  const float inv = l == 0.f ? 0.f : 1.0f / l;
+  Pack<T, V> out;
+#pragma unroll
+  for (int e = 0; e < V; ++e) out.v[e] = from_f32<T>(acc[e] * inv);
+  const int t = (int)(row % p.Lq), h = (int)(row / p.Lq % p.H), b = (int)(row / p.Lq / p.H);
+  *reinterpret_cast<Pack<T, V>*>(o + b * os.batch + h * os.head + t * os.row + lane * V) = out;
+  if (lane == 0 && p.lse != nullptr)
+    p.lse[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
+}
+
+// ------------------------------------------------------------------ host side
+// [Bt, H, L, D] as a 5-D map (64 columns, L, D / 64 column groups, H, Bt) with boxes of 128
+// rows of one head: D / 64 swizzled [128 x 64] sub-tiles, one behind the other.
+template <typename T>
+bool map_5d(CUtensorMap* m, const void* ptr, int D, int L, int H, int Bt, const bsa_strides& s) {
+  fwdtiles::EncodeTiledFn enc = fwdtiles::encode_fn();
+  if (!enc) return false;
+  auto bytes = [](int64_t v) { return (cuuint64_t)(v > 0 ? v * 2 : 16); };
+  cuuint64_t dims[5] = {64, (cuuint64_t)L, (cuuint64_t)(D / 64), (cuuint64_t)(s.head ? H : 1),
+                        (cuuint64_t)(s.batch ? Bt : 1)};
+  cuuint64_t strides[4] = {bytes(s.row), 128, bytes(s.head), bytes(s.batch)};
+  cuuint32_t box[5] = {64, 128, (cuuint32_t)(D / 64), 1, 1};
+  cuuint32_t es[5] = {1, 1, 1, 1, 1};
+  return enc(m, is_bf16<T>() ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 5,
+             const_cast<void*>(ptr), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Runs of key tiles per row tile: as many as fill the SMs, none below four tiles.
+int splits_of(int Bt, int H, int Lq, int Lk) {
+  const int64_t items = (int64_t)Bt * H * ceil_div(Lq, 2 * kBQ);
+  const int tiles = ceil_div(Lk, kBK);
+  const int64_t want = fwdtiles::sm_count() / items;
+  if (want < 2) return 1;
+  const int most = std::max(1, tiles / 4);
+  int splits = (int)std::min<int64_t>(want, most);
+  const int per = ceil_div(tiles, splits);
+  return ceil_div(tiles, per);
+}
+
+template <typename T, int D>
+cudaError_t run(const CrossArgs& a, cudaStream_t st) {
+  using C = Cfg<D>;
+  Params p;
+  p.Bt = a.Bt;
+  p.H = a.H;
+  p.share = a.H / a.Hkv;
+  p.Lq = a.Lq;
+  p.Lk = a.Lk;
+  p.q_tiles = ceil_div(a.Lq, 2 * kBQ);
+  p.splits = a.Lk > 0 ? splits_of(a.Bt, a.H, a.Lq, a.Lk) : 1;
+  p.tiles_per_split = ceil_div(std::max(ceil_div(a.Lk, kBK), 1), p.splits);
+  p.n_items = a.Bt * a.H * p.q_tiles * p.splits;
+  p.qb = a.qs.batch != 0;
+  p.qh = a.qs.head != 0;
+  p.kb = a.ks.batch != 0;
+  p.kh = a.ks.head != 0;
+  p.vb = a.vs.batch != 0;
+  p.vh = a.vs.head != 0;
+  p.key_len = a.key_len;
+  p.key_mask = a.key_mask;
+  p.scale_log2 = a.scale * 1.4426950408889634f;
+  p.lse = a.lse;
+  const int64_t rows = (int64_t)a.Bt * a.H * a.Lq;
+  p.part_ml = static_cast<float2*>(a.ws);
+  p.part_o = static_cast<float*>(a.ws) + (p.splits * rows * 2 + 3) / 4 * 4;
+  p.status = a.status;
+  p.wait_ns = kWaitTimeoutNs;
+  CUtensorMap tmQ, tmK, tmV, tmO;
+  bool ok = map_5d<T>(&tmQ, a.Q, D, a.Lq, a.H, a.Bt, a.qs) &&
+            map_5d<T>(&tmO, a.O, D, a.Lq, a.H, a.Bt, a.os);
+  if (a.Lk > 0)
+    ok = ok && map_5d<T>(&tmK, a.K, D, a.Lk, a.Hkv, a.Bt, a.ks) &&
+         map_5d<T>(&tmV, a.V, D, a.Lk, a.Hkv, a.Bt, a.vs);
+  else tmK = tmV = tmQ;  // no tile is loaded
+  if (!ok) return cudaErrorInvalidValue;
+  cudaError_t e = cudaFuncSetAttribute(k_cross<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       C::SMEM);
+  if (e != cudaSuccess) return e;
+  // setmaxnreg.inc waits for registers that the launch must hold
+  cudaFuncAttributes fa;
+  e = cudaFuncGetAttributes(&fa, k_cross<T, D>);
+  if (e != cudaSuccess) return e;
+  if (fa.numRegs * kThreads < 128 * kRegsControl + 256 * kRegsSoftmax)
+    return cudaErrorInvalidConfiguration;
+  k_cross<T, D><<<std::min(p.n_items, fwdtiles::sm_count()), kThreads, C::SMEM, st>>>(tmQ, tmK, tmV,
+                                                                                      tmO, p);
+  e = cudaGetLastError();
+  if (e != cudaSuccess || p.splits == 1) return e;
+  k_join<T, D><<<(unsigned)((rows + 3) / 4), 128, 0, st>>>(p, static_cast<T*>(a.O), a.os);
+  return cudaGetLastError();
+}
+
+}  // namespace cross
+
+size_t cross_workspace(int Bt, int H, int Lq, int Lk, int d) {
+  if (Lk <= 0) return 0;
+  const int splits = cross::splits_of(Bt, H, Lq, Lk);
+  if (splits == 1) return 0;
+  const size_t rows = (size_t)Bt * H * Lq;
+  return ((splits * rows * 2 + 3) / 4 * 4 + splits * rows * d) * sizeof(float);
+}
+
+cudaError_t launch_cross(const CrossArgs& a, cudaStream_t st) {
+  if (a.type == BSA_TYPE_BF16)
+    return a.d == 64 ? cross::run<__nv_bfloat16, 64>(a, st) : cross::run<__nv_bfloat16, 128>(a, st);
+  return a.d == 64 ? cross::run<__half, 64>(a, st) : cross::run<__half, 128>(a, st);
+}
+
+}  // namespace bsa

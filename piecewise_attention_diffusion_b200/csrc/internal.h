@@ -112,4 +112,24 @@ struct LinearArgs {
 size_t linear_workspace(int Bt, int L, int K, int N);
 cudaError_t launch_linear(const LinearArgs& a, cudaStream_t st);
 
+struct CrossArgs {
+  const void* Q;
+  bsa_strides qs;
+  const void* K;
+  bsa_strides ks;
+  const void* V;
+  bsa_strides vs;
+  int type, Bt, H, Hkv, Lq, Lk, d;
+  const int32_t* key_len;
+  const uint8_t* key_mask;
+  float scale;
+  void* O;
+  bsa_strides os;
+  float* lse;
+  void* ws;
+  int32_t* status;
+};
+size_t cross_workspace(int Bt, int H, int Lq, int Lk, int d);
+cudaError_t launch_cross(const CrossArgs& a, cudaStream_t st);
+
 }  // namespace bsa

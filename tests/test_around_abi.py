@@ -84,3 +84,43 @@ def _linear(x=P, xs=None, xh=1, w=P, w_row=0, bias=None, act=0, gate=None, r=Non
     (dict(Bt=2 ** 14, L=2 ** 15, N=2 ** 20), b.ERR_UNSUPPORTED)])
 def test_linear_refuses(kw, want):
     assert _linear(**kw) == want
+
+
+def _cross(q=P, qs=None, k=P, ks=None, v=P, vs=None, type=0, Bt=2, H=4, Hkv=2, Lq=8, Lk=16, d=64,
+           n=None, m=None, scale=0.0, o=P, os=None, lse=None, ws=P, ws_bytes=1 << 40):
+    return b.lib().bsa_cross_forward(q, qs, k, ks, v, vs, type, Bt, H, Hkv, Lq, Lk, d, n, m, scale,
+                                     o, os, lse, ws, ws_bytes, None, None)
+
+
+@pytest.mark.parametrize("kw,want", [
+    (dict(q=None), b.ERR_INVALID_ARG), (dict(k=None), b.ERR_INVALID_ARG),
+    (dict(v=None), b.ERR_INVALID_ARG), (dict(o=None), b.ERR_INVALID_ARG),
+    (dict(q=ODD), b.ERR_INVALID_ARG), (dict(k=ODD), b.ERR_INVALID_ARG),
+    (dict(o=ODD), b.ERR_INVALID_ARG), (dict(n=ctypes.c_void_p((1 << 20) + 2)), b.ERR_INVALID_ARG),
+    (dict(lse=ctypes.c_void_p((1 << 20) + 2)), b.ERR_INVALID_ARG),
+    (dict(Bt=0), b.ERR_INVALID_ARG), (dict(Lq=0), b.ERR_INVALID_ARG),
+    (dict(Lk=-1), b.ERR_INVALID_ARG), (dict(H=3), b.ERR_INVALID_ARG),
+    (dict(Hkv=0), b.ERR_INVALID_ARG), (dict(d=96), b.ERR_UNSUPPORTED),
+    (dict(type=2), b.ERR_UNSUPPORTED), (dict(type=-1), b.ERR_INVALID_ARG),
+    (dict(scale=-1.0), b.ERR_INVALID_ARG), (dict(scale=float("nan")), b.ERR_INVALID_ARG),
+    (dict(scale=float("inf")), b.ERR_INVALID_ARG),
+    (dict(qs=b.Strides(2048, 512, 68)), b.ERR_UNSUPPORTED),
+    (dict(qs=b.Strides(2048, 512, 0)), b.ERR_INVALID_ARG),
+    (dict(ks=b.Strides(2048, 1024, 0)), b.ERR_INVALID_ARG),
+    (dict(vs=b.Strides(2048, -64, 64)), b.ERR_INVALID_ARG),
+    (dict(os=b.Strides(0, 512, 64)), b.ERR_INVALID_ARG),
+    (dict(os=b.Strides(2048, 0, 64)), b.ERR_INVALID_ARG),
+    (dict(os=b.Strides(2048, 512, 0)), b.ERR_INVALID_ARG),
+    (dict(Lq=1 << 30), b.ERR_UNSUPPORTED), (dict(Bt=1 << 16, H=1 << 8), b.ERR_UNSUPPORTED),
+    (dict(Lq=1, Lk=8192, ws=None), b.ERR_WORKSPACE),
+    (dict(Lq=1, Lk=8192, ws_bytes=64), b.ERR_WORKSPACE)])
+def test_cross_refuses(kw, want):
+    assert _cross(**kw) == want
+
+
+def test_cross_workspace_sizes():
+    assert b.bsa_cross_workspace_bytes(1, 40, 40, 16384, 512, 128) == 0   # every SM has rows
+    assert b.bsa_cross_workspace_bytes(1, 2, 2, 1, 0, 64) == 0            # no key to split
+    assert b.bsa_cross_workspace_bytes(1, 2, 2, 1, 32768, 64) > 0
+    assert b.bsa_cross_workspace_bytes(1, 3, 2, 1, 32768, 64) == 0        # refused shapes
+    assert b.bsa_cross_workspace_bytes(1, 2, 2, 1, 32768, 96) == 0
