@@ -13,7 +13,7 @@
 // tensor work at BN = 256, where a CTA on its own would read 48 KB.
 //   warp 0     TMA producer (each CTA its half; both report to the leader's barrier);
 //   warp 1     MMA issuer (leader), TMEM allocation;
-//   warps 2-9  epilogue: two warps per TMEM lane quadrant, one for each half of the columns.
+//   warps 2..  epilogue: up to four warps per TMEM lane quadrant, each with its own columns.
 //              Per chunk of 32 columns: accumulators to registers, bias, activation,
 //              gate and residual in fp32, one rounding, then through a swizzled staging
 //              buffer to a TMA store (or coalesced 2-byte stores where Y's strides rule TMA
@@ -36,8 +36,6 @@ using namespace sm100;
 
 constexpr int kBM = 128;      // rows per CTA (256 per pair)
 constexpr int kBK = 64;       // columns of X and W per step: one 128-byte swizzled row
-constexpr int kEpiWarps = 8;
-constexpr int kThreads = 64 + 32 * kEpiWarps;
 constexpr int kCW = 32;        // columns per epilogue chunk: rows of 64 bytes in the staging buffer
 constexpr int kRowGroup = 8;  // row tiles that a sweep over the columns shares (L2 reuse)
 
@@ -59,23 +57,34 @@ struct Params {
   const T* res;
   T* y;
   View rv, yv;
-  int act;
   int tma_out;          // Y's base and strides allow TMA stores
   int vec_res;          // R's base and strides allow 16-byte loads
   int32_t* status;
   uint64_t wait_ns;
 };
 
-__device__ __forceinline__ float sigmoid_times(float z, float u) {  // z / (1 + e^-u)
-  return __fdividef(z, 1.0f + ex2(-1.4426950408889634f * u));
+// z / (1 + 2^-w) for a pair
+__device__ __forceinline__ float2 sigmoid_times(float2 z, float2 w) {
+  return make_float2(__fdividef(z.x, 1.0f + ex2(-w.x)), __fdividef(z.y, 1.0f + ex2(-w.y)));
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  return fma2(a, b, make_float2(-0.f, -0.f));
 }
 
-__device__ __forceinline__ float activate(float z, int act) {
-  if (act == BSA_ACT_GELU_TANH)  // (1 + tanh u) / 2 = 1 / (1 + e^-2u)
-    return sigmoid_times(z, 1.5957691216057308f * (z + 0.044715f * z * z * z));
-  // the complementary form keeps the tail of negative z, which 1 + erf would cancel
-  if (act == BSA_ACT_GELU_ERF) return 0.5f * z * erfcf(-0.70710678118654752f * z);
-  if (act == BSA_ACT_SILU) return sigmoid_times(z, z);
+// The activation is a template argument: with a branch per element nothing overlapped, and
+// the epilogue of a 128 x 256 tile took 40000 cycles where its products take 8300 (K = 1024).
+template <int kAct>
+__device__ __forceinline__ float2 activate(float2 z) {
+  constexpr float kLog2e = 1.4426950408889634f;
+  if (kAct == BSA_ACT_GELU_TANH) {  // (1 + tanh u) / 2 = 1 / (1 + e^-2u)
+    constexpr float c = 1.5957691216057308f * kLog2e, d = c * 0.044715f;
+    const float2 t = fma2(mul2(z, z), make_float2(d, d), make_float2(c, c));
+    return sigmoid_times(z, mul2(z, t));
+  }
+  if (kAct == BSA_ACT_GELU_ERF)  // the complementary form keeps the tail of negative z
+    return make_float2(0.5f * z.x * erfcf(-0.70710678118654752f * z.x),
+                       0.5f * z.y * erfcf(-0.70710678118654752f * z.y));
+  if (kAct == BSA_ACT_SILU) return sigmoid_times(z, mul2(z, make_float2(kLog2e, kLog2e)));
   return z;
 }
 
@@ -84,9 +93,14 @@ struct Cfg {
   static constexpr int A_BYTES = kBM * 128;
   static constexpr int B_BYTES = BN / 2 * 128;
   static constexpr int STAGE = A_BYTES + B_BYTES;
-  static constexpr int OUT = 2 * 32 * kCW * 2;  // staging bytes per epilogue warp, two chunks
-  static constexpr int NSTAGE = BN == 256 ? 6 : BN == 128 ? 7 : 9;
-  static constexpr int SMEM = NSTAGE * STAGE + kEpiWarps * OUT + 1024;
+  // epilogue warps: four (one per TMEM lane quadrant) for each of PARTS column ranges
+  static constexpr int PARTS = BN / kCW < 4 ? BN / kCW : 4;
+  static constexpr int COLS = BN / PARTS;
+  static constexpr int EPI = 4 * PARTS;
+  static constexpr int THREADS = 64 + 32 * EPI;
+  static constexpr int OUT = 32 * kCW * 2;  // staging bytes per epilogue warp: one chunk
+  static constexpr int NSTAGE = BN == 256 ? 5 : BN == 128 ? 6 : 9;
+  static constexpr int SMEM = NSTAGE * STAGE + EPI * OUT + 1024;
   static constexpr uint32_t TMEM = 2 * BN;              // two accumulators
 };
 
@@ -108,8 +122,8 @@ __device__ __forceinline__ void tile_of(const P& p, int t, int& m, int& n) {
   n = r / rows;
 }
 
-template <typename T, int BN>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+template <typename T, int BN, int kAct>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<BN>::THREADS, 1)
 k_linear(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW,
          const __grid_constant__ CUtensorMap tmY, const __grid_constant__ Params<T> p) {
   using C = Cfg<BN>;
@@ -120,7 +134,7 @@ k_linear(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtens
   __shared__ Barriers bars;
   __shared__ uint32_t tmem_base_sh;
   __shared__ int abort_sh;
-  __shared__ T cols_sh[kEpiWarps][kCW][2];  // bias and gate of a chunk's columns
+  __shared__ __align__(16) float bias_sh[C::EPI][kCW], gate_sh[C::EPI][kCW];  // of a chunk
 
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const uint32_t rank = cluster_rank();
@@ -132,7 +146,7 @@ k_linear(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtens
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bars.acc_full[i], 1);
-      mbar_init(&bars.acc_empty[i], 2 * kEpiWarps);
+      mbar_init(&bars.acc_empty[i], 2 * C::EPI);
     }
     mbar_init(&bars.done, 1);
     fence_barrier_init();
@@ -245,12 +259,12 @@ k_linear(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtens
     // -------------------------------------------------------------------- epilogue
     const int e = warp - 2;
     const int quad = warp % 4;                     // TMEM lane quadrant of this warp
-    const int half = e / 4;                        // its half of the columns
-    unsigned char* stage_out = smem + C::NSTAGE * C::STAGE + e * C::OUT;
+    const int part = e / 4;                        // its range of the columns
+    unsigned char* out = smem + C::NSTAGE * C::STAGE + e * C::OUT;
     const uint32_t empty_addr[2] = {cluster_addr(&bars.acc_empty[0], 0),
                                     cluster_addr(&bars.acc_empty[1], 0)};
     bool ok = true;
-    int it = 0, chunk = 0;
+    int it = 0;
     for (int t = first; t < tiles; t += step, ++it) {
       int m, n;
       tile_of(p, t, m, n);
@@ -259,72 +273,104 @@ k_linear(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtens
       const int row = row0 + lane;
       const bool live = row < p.L;
       const int acc = it & 1;
+      const int tile_col = n * BN + part * C::COLS;
+      // gate vector of this row (entries merged into one run of rows have several)
+      const int gate_of = p.gate != nullptr ? (b * p.L + min(row, p.L - 1)) / p.gate_rows : 0;
+      const bool one_gate = __all_sync(0xffffffffu, gate_of == __shfl_sync(0xffffffffu, gate_of, 0));
+      const T* gate = p.gate + (int64_t)gate_of * p.N;
+      const T* res_row = p.res + b * p.rv.batch + row * p.rv.row;
+      // what a chunk needs besides the accumulators: one column's bias and (shared) gate per
+      // lane, and 32 columns of the row's residual; asked for a chunk ahead
+      struct Ahead {
+        T bias, gate;
+        Pack<T, 8> res[kCW / 8];
+      } ahead;
+      auto fetch = [&](int col0) {
+        const bool in = col0 + lane < p.N;
+        ahead.bias = in && p.bias != nullptr ? p.bias[col0 + lane] : from_f32<T>(0.f);
+        ahead.gate = in && p.gate != nullptr && one_gate ? gate[col0 + lane] : from_f32<T>(1.f);
+      };
+      auto fetch_res = [&](int col) -> Pack<T, 8> {
+        const int head = col / p.rv.cols;
+        return *reinterpret_cast<const Pack<T, 8>*>(res_row + head * p.rv.head +
+                                                    (col - head * p.rv.cols));
+      };
+      const bool vec_res = p.vec_res && live;  // then 8 columns are all there or all not
+      const bool rows_here = row0 < p.L;
+      if (rows_here && tile_col < p.N) {
+        fetch(tile_col);
+#pragma unroll
+        for (int g = 0; g < kCW / 8; ++g)
+          if (vec_res && tile_col + g * 8 < p.N) ahead.res[g] = fetch_res(tile_col + g * 8);
+      }
       ok = mbar_wait(&bars.acc_full[acc], (it / 2) & 1, abort_flag, p.wait_ns);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
       tc_fence_after();
-      // gate vector of this row (entries merged into one run of rows have several)
-      const int gate_of = p.gate != nullptr ? (b * p.L + min(row, p.L - 1)) / p.gate_rows : 0;
-      const bool one_gate = __all_sync(0xffffffffu, gate_of == __shfl_sync(0xffffffffu, gate_of, 0));
 #pragma unroll 1
-      for (int c = 0; c < BN / 2; c += kCW) {
-        const int col0 = n * BN + half * (BN / 2) + c;
-        if (col0 >= p.N || row0 >= p.L) break;
+      for (int c = 0; c < C::COLS; c += kCW) {
+        const int col0 = tile_col + c;
+        if (col0 >= p.N || !rows_here) break;
         uint32_t r[kCW];
-        const uint32_t src = tmem + ((uint32_t)(quad * 32) << 16) + acc * BN + half * (BN / 2) + c;
-        tmem_ld32(src, r);
-        // the chunk's bias and (shared) gate, while the loads are under way
+        tmem_ld32(tmem + ((uint32_t)(quad * 32) << 16) + acc * BN + part * C::COLS + c, r);
+        bias_sh[e][lane] = to_f32(ahead.bias);
+        gate_sh[e][lane] = to_f32(ahead.gate);
+        const bool more = c + kCW < C::COLS && col0 + kCW < p.N;
+        if (more) fetch(col0 + kCW);
+        if (lane == 0) bulk_wait_read_all();  // the staging buffer's last store has read it
         __syncwarp();
-        {
-          const bool in = col0 + lane < p.N;
-          cols_sh[e][lane][0] =
-              in && p.bias != nullptr ? p.bias[col0 + lane] : from_f32<T>(0.f);
-          cols_sh[e][lane][1] = in && p.gate != nullptr && one_gate
-                                    ? p.gate[(int64_t)gate_of * p.N + col0 + lane]
-                                    : from_f32<T>(1.f);
+        if (p.res != nullptr && !p.vec_res) {
+          // a residual that 16-byte loads cannot take comes through the staging buffer, a
+          // row at a time across the lanes (places past the end repeat the last)
+          const int head = col0 / p.rv.cols;
+          const T* at = p.res + b * p.rv.batch + head * p.rv.head +
+                        (min(col0 + lane, p.N - 1) - head * p.rv.cols);
+#pragma unroll 8
+          for (int rr = 0; rr < 32; ++rr)
+            *reinterpret_cast<T*>(out + rr * kCW * 2 + ((lane / 8) ^ ((rr >> 1) & 3)) * 16 +
+                                  lane % 8 * 2) = at[min(row0 + rr, p.L - 1) * p.rv.row];
+          __syncwarp();
         }
-        __syncwarp();
         tmem_wait_ld();
-        const int head = col0 / p.rv.cols, hc = col0 - head * p.rv.cols;
-        const T* res = p.res == nullptr || !live
-                           ? nullptr
-                           : p.res + b * p.rv.batch + head * p.rv.head + row * p.rv.row + hc;
-        // of the two staging chunks, this one's last store has read it
-        unsigned char* out = stage_out + (chunk & 1) * (32 * kCW * 2);
-        if (lane == 0) bulk_wait_read_but_one();
-        __syncwarp();
-        ++chunk;
 #pragma unroll
         for (int g = 0; g < kCW / 8; ++g) {
-          float v[8];
+          const int col = col0 + g * 8;
+          // the 64-byte swizzle of the store's box: 16-byte piece g of row r sits at
+          // g ^ (r / 2 % 4)
+          Pack<T, 8>* slot = reinterpret_cast<Pack<T, 8>*>(out + lane * kCW * 2 +
+                                                           (g ^ ((lane >> 1) & 3)) * 16);
+          float2 v[4];
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const T* w = cols_sh[e][g * 8 + i];
-            v[i] = activate(__uint_as_float(r[g * 8 + i]) + to_f32(w[0]), p.act) * to_f32(w[1]);
-          }
-          if (p.gate != nullptr && !one_gate) {
-            const T* gate = p.gate + (int64_t)gate_of * p.N + col0 + g * 8;
+          for (int i = 0; i < 4; ++i)
+            v[i] = activate<kAct>(add2(make_float2(__uint_as_float(r[g * 8 + 2 * i]),
+                                                   __uint_as_float(r[g * 8 + 2 * i + 1])),
+                                       *reinterpret_cast<float2*>(&bias_sh[e][g * 8 + 2 * i])));
+          if (p.gate != nullptr) {
+            if (one_gate) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-              if (col0 + g * 8 + i < p.N) v[i] *= to_f32(gate[i]);
-          }
-          if (res != nullptr) {
-            if (p.vec_res && col0 + g * 8 + 8 <= p.N) {
-              const Pack<T, 8> w = *reinterpret_cast<const Pack<T, 8>*>(res + g * 8);
-#pragma unroll
-              for (int i = 0; i < 8; ++i) v[i] += to_f32(w.v[i]);
+              for (int i = 0; i < 4; ++i)
+                v[i] = mul2(v[i], *reinterpret_cast<float2*>(&gate_sh[e][g * 8 + 2 * i]));
             } else {
 #pragma unroll
-              for (int i = 0; i < 8; ++i)
-                if (col0 + g * 8 + i < p.N) v[i] += to_f32(res[g * 8 + i]);
+              for (int i = 0; i < 4; ++i)
+                v[i] = mul2(v[i], make_float2(to_f32(gate[min(col + 2 * i, p.N - 1)]),
+                                              to_f32(gate[min(col + 2 * i + 1, p.N - 1)])));
             }
+          }
+          if (p.res != nullptr) {
+            const Pack<T, 8> w = p.vec_res ? ahead.res[g] : *slot;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              v[i] = add2(v[i], make_float2(to_f32(w.v[2 * i]), to_f32(w.v[2 * i + 1])));
+            if (more && vec_res && col + kCW < p.N) ahead.res[g] = fetch_res(col + kCW);
           }
           Pack<T, 8> o;
 #pragma unroll
-          for (int i = 0; i < 8; ++i) o.v[i] = from_f32<T>(v[i]);
-          // the 64-byte swizzle of the store's box: 16-byte piece g of row r sits at
-          // g ^ (r / 2 % 4)
-          *reinterpret_cast<Pack<T, 8>*>(out + lane * kCW * 2 + (g ^ ((lane >> 1) & 3)) * 16) = o;
+          for (int i = 0; i < 4; ++i) {
+            o.v[2 * i] = from_f32<T>(v[i].x);
+            o.v[2 * i + 1] = from_f32<T>(v[i].y);
+          }
+          *slot = o;
         }
         const int yhead = col0 / p.yv.cols, yc = col0 - yhead * p.yv.cols;
         if (p.tma_out) {
@@ -400,7 +446,7 @@ bool whole16(const void* ptr, const bsa_strides& s) {
          s.row % 8 == 0;
 }
 
-template <typename T, int BN>
+template <typename T, int BN, int kAct>
 cudaError_t run(const LinearArgs& a, cudaStream_t st) {
   using C = Cfg<BN>;
   Params<T> p;
@@ -423,9 +469,8 @@ cudaError_t run(const LinearArgs& a, cudaStream_t st) {
   p.y = static_cast<T*>(a.Y);
   p.rv = View{a.rs.batch, a.rs.head, a.rs.row, dy};
   p.yv = View{a.ys.batch, a.ys.head, a.ys.row, dy};
-  p.act = a.act;
   p.tma_out = whole16(a.Y, a.ys);
-  p.vec_res = a.R != nullptr && whole16(a.R, a.rs);
+  p.vec_res = a.R != nullptr && a.N % 8 == 0 && whole16(a.R, a.rs);
   p.status = a.status;
   p.wait_ns = kWaitTimeoutNs;
   CUtensorMap tmX, tmW, tmY;
@@ -434,23 +479,31 @@ cudaError_t run(const LinearArgs& a, cudaStream_t st) {
   if (p.tma_out) ok = ok && map_4d<T>(&tmY, a.Y, dy, a.L, a.y_heads, a.Bt, a.ys, kCW, 32);
   else tmY = tmX;
   if (!ok) return cudaErrorInvalidValue;
-  cudaError_t e = cudaFuncSetAttribute(k_linear<T, BN>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+  cudaError_t e = cudaFuncSetAttribute(k_linear<T, BN, kAct>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        C::SMEM);
   if (e != cudaSuccess) return e;
   const int64_t tiles = (int64_t)p.m_tiles * p.n_tiles;
   const int pairs = (int)std::min<int64_t>(tiles, fwdtiles::sm_count() / 2);
-  k_linear<T, BN><<<2 * pairs, kThreads, C::SMEM, st>>>(tmX, tmW, tmY, p);
+  k_linear<T, BN, kAct><<<2 * pairs, C::THREADS, C::SMEM, st>>>(tmX, tmW, tmY, p);
   return cudaGetLastError();
+}
+
+template <typename T, int kAct>
+cudaError_t by_width(const LinearArgs& a, cudaStream_t st) {
+  const int pairs = fwdtiles::sm_count() / 2;
+  const int64_t m = (int64_t)a.Bt * ceil_div(a.L, 2 * kBM);
+  // the widest tile that still gives every pair of SMs one
+  if (m * ceil_div(a.N, 256) >= pairs) return run<T, 256, kAct>(a, st);
+  if (m * ceil_div(a.N, 128) >= pairs) return run<T, 128, kAct>(a, st);
+  return run<T, 64, kAct>(a, st);
 }
 
 template <typename T>
 cudaError_t dispatch(const LinearArgs& a, cudaStream_t st) {
-  const int pairs = fwdtiles::sm_count() / 2;
-  const int64_t m = (int64_t)a.Bt * ceil_div(a.L, 2 * kBM);
-  // the widest tile that still gives every pair of SMs one
-  if (m * ceil_div(a.N, 256) >= pairs) return run<T, 256>(a, st);
-  if (m * ceil_div(a.N, 128) >= pairs) return run<T, 128>(a, st);
-  return run<T, 64>(a, st);
+  if (a.act == BSA_ACT_GELU_TANH) return by_width<T, BSA_ACT_GELU_TANH>(a, st);
+  if (a.act == BSA_ACT_GELU_ERF) return by_width<T, BSA_ACT_GELU_ERF>(a, st);
+  if (a.act == BSA_ACT_SILU) return by_width<T, BSA_ACT_SILU>(a, st);
+  return by_width<T, BSA_ACT_NONE>(a, st);
 }
 
 }  // namespace linear
