@@ -23,70 +23,15 @@
 // BSA_ERR_TIMEOUT.
 #include <algorithm>
 
-#include "common.cuh"
-#include "forward_tiles.cuh"
-#include "internal.h"
+#include "linear_common.cuh"
 #include "sm100_pair.cuh"
-#include "types.cuh"
 
 namespace bsa {
 namespace linear {
 
-using namespace sm100;
-
 constexpr int kBM = 128;      // rows per CTA (256 per pair)
-constexpr int kBK = 64;       // columns of X and W per step: one 128-byte swizzled row
 constexpr int kCW = 32;        // columns per epilogue chunk: rows of 64 bytes in the staging buffer
 constexpr int kRowGroup = 8;  // row tiles that a sweep over the columns shares (L2 reuse)
-
-// What the epilogue needs of a [Bt, H, L, d] operand with H * d = N columns.
-struct View {
-  int64_t batch, head, row;
-  int cols;  // d
-};
-
-template <typename T>
-struct Params {
-  int Bt, L, K, N;
-  int gate_rows;        // rows of an entry that share one gate vector
-  int x_steps;          // 64-column steps per head of X
-  int xb, xh;           // 0 where X's batch or head stride is 0 (one copy for all)
-  int k_steps, row_tiles, m_tiles, n_tiles;
-  const T* bias;
-  const T* gate;
-  const T* res;
-  T* y;
-  View rv, yv;
-  int tma_out;          // Y's base and strides allow TMA stores
-  int vec_res;          // R's base and strides allow 16-byte loads
-  int32_t* status;
-  uint64_t wait_ns;
-};
-
-// z / (1 + 2^-w) for a pair
-__device__ __forceinline__ float2 sigmoid_times(float2 z, float2 w) {
-  return make_float2(__fdividef(z.x, 1.0f + ex2(-w.x)), __fdividef(z.y, 1.0f + ex2(-w.y)));
-}
-__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
-  return fma2(a, b, make_float2(-0.f, -0.f));
-}
-
-// The activation is a template argument: with a branch per element nothing overlapped, and
-// the epilogue of a 128 x 256 tile took 40000 cycles where its products take 8300 (K = 1024).
-template <int kAct>
-__device__ __forceinline__ float2 activate(float2 z) {
-  constexpr float kLog2e = 1.4426950408889634f;
-  if (kAct == BSA_ACT_GELU_TANH) {  // (1 + tanh u) / 2 = 1 / (1 + e^-2u)
-    constexpr float c = 1.5957691216057308f * kLog2e, d = c * 0.044715f;
-    const float2 t = fma2(mul2(z, z), make_float2(d, d), make_float2(c, c));
-    return sigmoid_times(z, mul2(z, t));
-  }
-  if (kAct == BSA_ACT_GELU_ERF)  // the complementary form keeps the tail of negative z
-    return make_float2(0.5f * z.x * erfcf(-0.70710678118654752f * z.x),
-                       0.5f * z.y * erfcf(-0.70710678118654752f * z.y));
-  if (kAct == BSA_ACT_SILU) return sigmoid_times(z, mul2(z, make_float2(kLog2e, kLog2e)));
-  return z;
-}
 
 template <int BN>
 struct Cfg {
@@ -166,95 +111,103 @@ k_linear(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtens
   tc_fence_after();
   const uint32_t tmem = tmem_base_sh;
   volatile int* abort_flag = &abort_sh;
-  const int tiles = p.m_tiles * p.n_tiles;
-  const int first = blockIdx.x / 2, step = gridDim.x / 2;
+  const int group = blockIdx.x / 2, groups = gridDim.x / 2;
+  // k_finish may take its place now; it waits for this grid before it reads a sum
+  if (p.split) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   if (warp == 0) {
     // ---------------------------------------------------------------- TMA producer
-    if (lane == 0) {
-      int stage = 0;
-      uint32_t phase = 0, issued = 0;
-      bool ok = true;
-      for (int t = first; t < tiles && ok; t += step) {
-        int m, n;
-        tile_of(p, t, m, n);
-        const int b = m / p.row_tiles;
-        const int row = (m % p.row_tiles) * 2 * kBM + (int)rank * kBM;
-        const int wrow = n * BN + (int)rank * (BN / 2);
-        int z = 0, x = 0;  // head and column of X at this step
-        for (int k = 0; k < p.k_steps; ++k) {
-          ok = mbar_wait(&bars.empty[stage], phase ^ 1, abort_flag, p.wait_ns);
-          if (!ok) break;
-          const uint32_t bar = cluster_addr(&bars.full[stage], 0);
+    int stage = 0;
+    uint32_t phase = 0, issued = 0;
+    bool ok = true;
+    const uint32_t full0 = cluster_addr(&bars.full[0], 0);  // the leader's barriers
+    WorkIter iter(p, group, groups);
+    for (Work w; ok && iter.next(p, w);) {
+      int m, n;
+      tile_of(p, w.tile, m, n);
+      const int b = m / p.row_tiles;
+      const int row = (m % p.row_tiles) * 2 * kBM + (int)rank * kBM;
+      const int wrow = n * BN + (int)rank * (BN / 2);
+      int z = w.k0 / p.x_steps, x = w.k0 % p.x_steps;  // head and column step of X
+      for (int k = w.k0; k < w.k1; ++k) {
+        ok = mbar_wait_warp(&bars.empty[stage], phase ^ 1, abort_flag, p.wait_ns);
+        if (!ok) break;
+        if (elect_one()) {
           if (rank == 0) mbar_arrive_expect_tx(&bars.full[stage], 2 * C::STAGE);
           unsigned char* dst = smem + stage * C::STAGE;
-          tma_load_4d_pair(dst, &tmX, bar, x * kBK, row, z * p.xh, b * p.xb);
-          tma_load_2d_pair(dst + C::A_BYTES, &tmW, bar, k * kBK, wrow);
-          ++issued;
-          if (++x == p.x_steps) {
-            x = 0;
-            ++z;
-          }
-          if (++stage == C::NSTAGE) {
-            stage = 0;
-            phase ^= 1u;
-          }
+          tma_load_4d_pair(dst, &tmX, full0 + stage * 8, x * kBK, row, z * p.xh, b * p.xb);
+          tma_load_2d_pair(dst + C::A_BYTES, &tmW, full0 + stage * 8, k * kBK, wrow);
+        }
+        __syncwarp();
+        ++issued;
+        if (++x == p.x_steps) {
+          x = 0;
+          ++z;
+        }
+        if (++stage == C::NSTAGE) {
+          stage = 0;
+          phase ^= 1u;
         }
       }
-      // The peer's copies report to the leader, whose last waits below see them land; the
-      // cluster barrier at the end keeps the peer until then.
-      if (!ok && rank == 0) {
-        const uint64_t t0 = globaltimer_ns();
-        const uint32_t from = issued > (uint32_t)C::NSTAGE ? issued - C::NSTAGE : 0;
-        for (uint32_t r = from; r < issued; ++r)
-          while (!mbar_try_wait(&bars.full[r % C::NSTAGE], (r / C::NSTAGE) & 1) &&
-                 globaltimer_ns() - t0 < 100000000ull) {
-          }
-      }
     }
-    __syncwarp();
+    // The peer's copies report to the leader, whose last waits below see them land; the
+    // cluster barrier at the end keeps the peer until then.
+    if (!ok && rank == 0) {
+      const uint64_t t0 = globaltimer_ns();
+      const uint32_t from = issued > (uint32_t)C::NSTAGE ? issued - C::NSTAGE : 0;
+      for (uint32_t r = from; r < issued; ++r)
+        while (!mbar_try_wait(&bars.full[r % C::NSTAGE], (r / C::NSTAGE) & 1) &&
+               globaltimer_ns() - t0 < 100000000ull) {
+        }
+      __syncwarp();
+    }
   } else if (warp == 1) {
     // ------------------------------------------------------------------ MMA issuer
-    if (lane == 0 && rank == 0) {
+    if (rank == 0) {
       // D fp32; A and B both T, K-major; M = 256 over the pair
       constexpr uint32_t fmt = sizeof(T) == 2 && is_bf16<T>() ? 1u : 0u;
       constexpr uint32_t idesc = (1u << 4) | (fmt << 7) | (fmt << 10) | ((uint32_t)(BN >> 3) << 17) |
                                  ((uint32_t)(2 * kBM >> 4) << 24);
+      const uint64_t desc0 = smem_desc_sw128(smem_u32(smem), 16, 1024);
       int stage = 0, it = 0;
       uint32_t phase = 0;
       bool ok = true;
-      for (int t = first; t < tiles && ok; t += step, ++it) {
+      WorkIter iter(p, group, groups);
+      for (Work w; ok && iter.next(p, w); ++it) {
         const int acc = it & 1;
-        if (it >= 2) ok = mbar_wait(&bars.acc_empty[acc], (it / 2 - 1) & 1, abort_flag, p.wait_ns);
+        if (it >= 2)
+          ok = mbar_wait_warp(&bars.acc_empty[acc], (it / 2 - 1) & 1, abort_flag, p.wait_ns);
         if (!ok) break;
         tc_fence_after();
-        for (int k = 0; k < p.k_steps; ++k) {
-          ok = mbar_wait(&bars.full[stage], phase, abort_flag, p.wait_ns);
+        for (int k = w.k0; k < w.k1; ++k) {
+          ok = mbar_wait_warp(&bars.full[stage], phase, abort_flag, p.wait_ns);
           if (!ok) break;
           tc_fence_after();
-          const uint32_t addr = smem_u32(smem + stage * C::STAGE);
-          const uint64_t a0 = smem_desc_sw128(addr, 16, 1024);
-          const uint64_t b0 = smem_desc_sw128(addr + C::A_BYTES, 16, 1024);
+          if (elect_one()) {
+            const uint64_t a0 = desc0 + (uint64_t)(stage * (C::STAGE >> 4));
+            const uint64_t b0 = a0 + (C::A_BYTES >> 4);
 #pragma unroll
-          for (int j = 0; j < kBK / 16; ++j)
-            mma_ss_pair(tmem + acc * BN, a0 + j * 2, b0 + j * 2, idesc, (k | j) ? 1u : 0u);
-          mma_commit_pair(&bars.empty[stage]);
+            for (int j = 0; j < kBK / 16; ++j)
+              mma_ss_pair(tmem + acc * BN, a0 + j * 2, b0 + j * 2, idesc, k > w.k0 || j > 0 ? 1u : 0u);
+            mma_commit_pair(&bars.empty[stage]);
+            if (k + 1 == w.k1) mma_commit_pair(&bars.acc_full[acc]);
+          }
+          __syncwarp();
           if (++stage == C::NSTAGE) {
             stage = 0;
             phase ^= 1u;
           }
         }
-        if (ok) mma_commit_pair(&bars.acc_full[acc]);
       }
       if (!ok) {
         // the MMAs already issued end before TMEM is freed
-        mma_commit_pair(&bars.done);
+        if (elect_one()) mma_commit_pair(&bars.done);
         const uint64_t t0 = globaltimer_ns();
         while (!mbar_try_wait(&bars.done, 0) && globaltimer_ns() - t0 < 100000000ull) {
         }
+        __syncwarp();
       }
     }
-    __syncwarp();
   } else {
     // -------------------------------------------------------------------- epilogue
     const int e = warp - 2;
@@ -265,9 +218,10 @@ k_linear(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtens
                                     cluster_addr(&bars.acc_empty[1], 0)};
     bool ok = true;
     int it = 0;
-    for (int t = first; t < tiles; t += step, ++it) {
+    WorkIter iter(p, group, groups);
+    for (Work w; iter.next(p, w); ++it) {
       int m, n;
-      tile_of(p, t, m, n);
+      tile_of(p, w.tile, m, n);
       const int b = m / p.row_tiles;
       const int row0 = (m % p.row_tiles) * 2 * kBM + (int)rank * kBM + quad * 32;
       const int row = row0 + lane;
@@ -297,8 +251,25 @@ k_linear(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtens
       };
       const bool vec_res = p.vec_res && live;  // then 8 columns are all there or all not
       const bool rows_here = row0 < p.L;
-      if (rows_here && tile_col < p.N) {
+      const bool whole = !partial(p, w);
+      // a residual that 16-byte loads cannot take comes through the staging buffer, a row at a
+      // time across the lanes (places past the end repeat the last)
+      auto stage_res = [&](int col0) {
+        const int head = col0 / p.rv.cols;
+        const T* at = p.res + b * p.rv.batch + head * p.rv.head +
+                      (min(col0 + lane, p.N - 1) - head * p.rv.cols);
+#pragma unroll 16
+        for (int rr = 0; rr < 32; ++rr)
+          *reinterpret_cast<T*>(out + rr * kCW * 2 + ((lane / 8) ^ ((rr >> 1) & 3)) * 16 +
+                                lane % 8 * 2) = at[min(row0 + rr, p.L - 1) * p.rv.row];
+      };
+      if (whole && rows_here && tile_col < p.N) {
         fetch(tile_col);
+        if (p.res != nullptr && !p.vec_res) {
+          if (lane == 0) bulk_wait_read_all();
+          __syncwarp();
+          stage_res(tile_col);
+        }
 #pragma unroll
         for (int g = 0; g < kCW / 8; ++g)
           if (vec_res && tile_col + g * 8 < p.N) ahead.res[g] = fetch_res(tile_col + g * 8);
@@ -313,24 +284,27 @@ k_linear(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtens
         if (col0 >= p.N || !rows_here) break;
         uint32_t r[kCW];
         tmem_ld32(tmem + ((uint32_t)(quad * 32) << 16) + acc * BN + part * C::COLS + c, r);
+        if (!whole) {  // a partial sum: 128 bytes of the slot's row
+          tmem_wait_ld();
+          float* at = slot_of(p, w, group, BN) +
+                      (int64_t)(row - (m % p.row_tiles) * 2 * kBM) * BN + part * C::COLS + c;
+          if (live)
+#pragma unroll
+            for (int i = 0; i < kCW; i += 8)
+              asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(at + i),
+                           "r"(r[i]), "r"(r[i + 1]), "r"(r[i + 2]), "r"(r[i + 3]), "r"(r[i + 4]),
+                           "r"(r[i + 5]), "r"(r[i + 6]), "r"(r[i + 7])
+                           : "memory");
+          continue;
+        }
         bias_sh[e][lane] = to_f32(ahead.bias);
         gate_sh[e][lane] = to_f32(ahead.gate);
         const bool more = c + kCW < C::COLS && col0 + kCW < p.N;
         if (more) fetch(col0 + kCW);
         if (lane == 0) bulk_wait_read_all();  // the staging buffer's last store has read it
         __syncwarp();
-        if (p.res != nullptr && !p.vec_res) {
-          // a residual that 16-byte loads cannot take comes through the staging buffer, a
-          // row at a time across the lanes (places past the end repeat the last)
-          const int head = col0 / p.rv.cols;
-          const T* at = p.res + b * p.rv.batch + head * p.rv.head +
-                        (min(col0 + lane, p.N - 1) - head * p.rv.cols);
-#pragma unroll 8
-          for (int rr = 0; rr < 32; ++rr)
-            *reinterpret_cast<T*>(out + rr * kCW * 2 + ((lane / 8) ^ ((rr >> 1) & 3)) * 16 +
-                                  lane % 8 * 2) = at[min(row0 + rr, p.L - 1) * p.rv.row];
-          __syncwarp();
-        }
+        if (c > 0 && p.res != nullptr && !p.vec_res) stage_res(col0);
+        __syncwarp();
         tmem_wait_ld();
 #pragma unroll
         for (int g = 0; g < kCW / 8; ++g) {
@@ -407,108 +381,171 @@ k_linear(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtens
   }
 }
 
+// The tiles whose sums several groups share: slots added in the order of the steps, then the
+// same epilogue. A thread takes four columns of a row; tiles that one group summed whole are
+// already written.
+template <typename T, int kAct>
+__global__ void __launch_bounds__(256)
+k_finish(const Params<T> p, int few, int groups, int cols, int rows) {
+  // the groups [g0, g1) that share this block's tile
+  const int tile = blockIdx.x, units = p.m_tiles * p.n_tiles * p.k_steps;
+  const int u0 = tile * p.k_steps, u1 = u0 + p.k_steps;
+  int g0 = min((int)((int64_t)u0 * groups / units), groups - 1);
+  while (first_unit(units, groups, g0) > u0) --g0;
+  while (first_unit(units, groups, g0 + 1) <= u0) ++g0;
+  int g1 = g0 + 1;
+  while (first_unit(units, groups, g1) < u1) ++g1;
+  int m, n;
+  if (few) {
+    n = tile / p.m_tiles;
+    m = tile % p.m_tiles;
+  } else {
+    tile_of(p, tile, m, n);
+  }
+  const int id = blockIdx.y * 256 + threadIdx.x;
+  const int r = id / (cols / 4), c = id % (cols / 4) * 4;
+  const int b = m / p.row_tiles, row = (m % p.row_tiles) * rows + r, col = n * cols + c;
+  const bool mine = g1 - g0 > 1 && r < p.part_rows && row < p.L && col < p.N;
+  const int live = min(4, p.N - col);
+  float bias[4] = {}, gate[4], res[4] = {};
+  const T* at_gate = p.gate + (int64_t)((b * p.L + row) / p.gate_rows) * p.N + col;
+  const int rhead = col / p.rv.cols, yhead = col / p.yv.cols;
+  const T* at_res = p.res + b * p.rv.batch + rhead * p.rv.head + row * p.rv.row + (col - rhead * p.rv.cols);
+  T* y = p.y + b * p.yv.batch + yhead * p.yv.head + row * p.yv.row + (col - yhead * p.yv.cols);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const bool in = mine && i < live;
+    if (in && p.bias != nullptr) bias[i] = to_f32(p.bias[col + i]);
+    gate[i] = in && p.gate != nullptr ? to_f32(at_gate[i]) : 1.f;
+    if (in && p.res != nullptr) res[i] = to_f32(at_res[i]);
+  }
+  // every block waits, also one with nothing to add: this grid must not end before the one
+  // that sums
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (!mine) return;
+  const float* at = p.part + ((int64_t)2 * g0 * p.part_rows + r) * cols + c;
+  const int64_t slot = (int64_t)p.part_rows * cols;
+  // the first group's slot is its second one (its run begins at or before the tile), a later
+  // group's its first one, as slot_of has it
+  float4 sum = *reinterpret_cast<const float4*>(at + slot);
+#pragma unroll 4
+  for (int g = 1; g < g1 - g0; ++g) {
+    const float4 v = *reinterpret_cast<const float4*>(at + 2 * g * slot);
+    sum.x += v.x;
+    sum.y += v.y;
+    sum.z += v.z;
+    sum.w += v.w;
+  }
+  const float v[4] = {sum.x, sum.y, sum.z, sum.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float z = v[i] + bias[i];
+    if (i < live)
+      y[i] = from_f32<T>(activate<kAct>(make_float2(z, z)).x * gate[i] + res[i]);
+  }
+}
+
 // ------------------------------------------------------------------ host side
-// A [Bt][H][L][d] operand as a 4-D map with boxes of box_cols x box_rows.
-template <typename T>
-bool map_4d(CUtensorMap* m, const void* ptr, int d, int L, int H, int Bt, const bsa_strides& s,
-            int box_cols, int box_rows) {
-  fwdtiles::EncodeTiledFn enc = fwdtiles::encode_fn();
-  if (!enc) return false;
-  // a dimension that is never stepped over still needs a legal stride
-  auto bytes = [](int64_t v) { return (cuuint64_t)(v > 0 ? v * 2 : 16); };
-  cuuint64_t dims[4] = {(cuuint64_t)d, (cuuint64_t)L, (cuuint64_t)(s.head ? H : 1),
-                        (cuuint64_t)(s.batch ? Bt : 1)};
-  cuuint64_t strides[3] = {bytes(s.row), bytes(s.head), bytes(s.batch)};
-  cuuint32_t box[4] = {(cuuint32_t)box_cols, (cuuint32_t)box_rows, 1, 1};
-  cuuint32_t es[4] = {1, 1, 1, 1};
-  return enc(m, is_bf16<T>() ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4,
-             const_cast<void*>(ptr), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
-             box_cols == kBK ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
-             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-template <typename T>
-bool map_w(CUtensorMap* m, const void* ptr, int K, int N, int64_t row, int box_rows) {
-  fwdtiles::EncodeTiledFn enc = fwdtiles::encode_fn();
-  if (!enc) return false;
-  cuuint64_t dims[2] = {(cuuint64_t)K, (cuuint64_t)N};
-  cuuint64_t strides[1] = {(cuuint64_t)(N > 1 ? row * 2 : 16)};
-  cuuint32_t box[2] = {kBK, (cuuint32_t)box_rows};
-  cuuint32_t es[2] = {1, 1};
-  return enc(m, is_bf16<T>() ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2,
-             const_cast<void*>(ptr), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
-             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-bool whole16(const void* ptr, const bsa_strides& s) {
-  return (reinterpret_cast<uintptr_t>(ptr) & 15u) == 0 && s.batch % 8 == 0 && s.head % 8 == 0 &&
-         s.row % 8 == 0;
-}
-
 template <typename T, int BN, int kAct>
-cudaError_t run(const LinearArgs& a, cudaStream_t st) {
+cudaError_t run_pair(const LinearArgs& a, const Plan& plan, cudaStream_t st) {
   using C = Cfg<BN>;
-  Params<T> p;
-  p.Bt = a.Bt;
-  p.L = a.L;
-  p.K = a.K;
-  p.N = a.N;
-  p.gate_rows = a.gate_rows;
+  const Params<T> p = params_of<T>(a, plan);
   const int dx = a.K / a.x_heads, dy = a.N / a.y_heads;
-  p.x_steps = ceil_div(dx, kBK);
-  p.xb = a.xs.batch != 0;
-  p.xh = a.xs.head != 0;
-  p.k_steps = p.x_steps * a.x_heads;
-  p.row_tiles = ceil_div(a.L, 2 * kBM);
-  p.m_tiles = a.Bt * p.row_tiles;
-  p.n_tiles = ceil_div(a.N, BN);
-  p.bias = static_cast<const T*>(a.bias);
-  p.gate = static_cast<const T*>(a.gate);
-  p.res = static_cast<const T*>(a.R);
-  p.y = static_cast<T*>(a.Y);
-  p.rv = View{a.rs.batch, a.rs.head, a.rs.row, dy};
-  p.yv = View{a.ys.batch, a.ys.head, a.ys.row, dy};
-  p.tma_out = whole16(a.Y, a.ys);
-  p.vec_res = a.R != nullptr && a.N % 8 == 0 && whole16(a.R, a.rs);
-  p.status = a.status;
-  p.wait_ns = kWaitTimeoutNs;
   CUtensorMap tmX, tmW, tmY;
   bool ok = map_4d<T>(&tmX, a.X, dx, a.L, a.x_heads, a.Bt, a.xs, kBK, kBM) &&
             map_w<T>(&tmW, a.W, a.K, a.N, a.w_row, BN / 2);
   if (p.tma_out) ok = ok && map_4d<T>(&tmY, a.Y, dy, a.L, a.y_heads, a.Bt, a.ys, kCW, 32);
   else tmY = tmX;
   if (!ok) return cudaErrorInvalidValue;
-  cudaError_t e = cudaFuncSetAttribute(k_linear<T, BN, kAct>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       C::SMEM);
+  cudaError_t e = cudaFuncSetAttribute(k_linear<T, BN, kAct>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
   if (e != cudaSuccess) return e;
-  const int64_t tiles = (int64_t)p.m_tiles * p.n_tiles;
-  const int pairs = (int)std::min<int64_t>(tiles, fwdtiles::sm_count() / 2);
-  k_linear<T, BN, kAct><<<2 * pairs, C::THREADS, C::SMEM, st>>>(tmX, tmW, tmY, p);
+  k_linear<T, BN, kAct><<<2 * plan.groups, C::THREADS, C::SMEM, st>>>(tmX, tmW, tmY, p);
   return cudaGetLastError();
 }
 
 template <typename T, int kAct>
-cudaError_t by_width(const LinearArgs& a, cudaStream_t st) {
-  const int pairs = fwdtiles::sm_count() / 2;
-  const int64_t m = (int64_t)a.Bt * ceil_div(a.L, 2 * kBM);
-  // the widest tile that still gives every pair of SMs one
-  if (m * ceil_div(a.N, 256) >= pairs) return run<T, 256, kAct>(a, st);
-  if (m * ceil_div(a.N, 128) >= pairs) return run<T, 128, kAct>(a, st);
-  return run<T, 64, kAct>(a, st);
+cudaError_t run(const LinearArgs& a, const Plan& plan, cudaStream_t st) {
+  cudaError_t e = plan.few           ? run_few<T>(a, plan, st)
+                  : plan.cols == 256 ? run_pair<T, 256, kAct>(a, plan, st)
+                  : plan.cols == 128 ? run_pair<T, 128, kAct>(a, plan, st)
+                                     : run_pair<T, 64, kAct>(a, plan, st);
+  if (e != cudaSuccess || !plan.split) return e;
+  const Params<T> p = params_of<T>(a, plan);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(p.m_tiles * p.n_tiles),
+                     (unsigned)ceil_div(p.part_rows * (plan.cols / 4), 256));
+  cfg.blockDim = dim3(256);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, k_finish<T, kAct>, p, (int)plan.few, plan.groups, plan.cols,
+                            plan.rows);
 }
 
 template <typename T>
 cudaError_t dispatch(const LinearArgs& a, cudaStream_t st) {
-  if (a.act == BSA_ACT_GELU_TANH) return by_width<T, BSA_ACT_GELU_TANH>(a, st);
-  if (a.act == BSA_ACT_GELU_ERF) return by_width<T, BSA_ACT_GELU_ERF>(a, st);
-  if (a.act == BSA_ACT_SILU) return by_width<T, BSA_ACT_SILU>(a, st);
-  return by_width<T, BSA_ACT_NONE>(a, st);
+  const int k_steps = ceil_div(a.K / a.x_heads, kBK) * a.x_heads;
+  const Plan plan = plan_of(a.Bt, a.L, k_steps, a.N);
+  if (a.act == BSA_ACT_GELU_TANH) return run<T, BSA_ACT_GELU_TANH>(a, plan, st);
+  if (a.act == BSA_ACT_GELU_ERF) return run<T, BSA_ACT_GELU_ERF>(a, plan, st);
+  if (a.act == BSA_ACT_SILU) return run<T, BSA_ACT_SILU>(a, plan, st);
+  return run<T, BSA_ACT_NONE>(a, plan, st);
+}
+
+// The plan of least estimated time, in microseconds. The constants were fitted to calls of 4 to
+// 4096 rows, K 1024 to 10240 and N 1024 to 16384 (each plan timed on each size): a step of a
+// tile, what a tile and a call cost besides, and for sums shared between groups the second
+// kernel and its traffic per output. Whole tiles win where they fill the SMs (1024 x 1024 x
+// 16384, 4 rows: 6.8 against 7.9), sharing where they do not (5120 x 5120, 4 rows: 13.1 against
+// 20.9; 256 rows, K 10240, N 1024: 18 against 34) or where a last wave would be nearly empty
+// and the output is small.
+Plan plan_of(int Bt, int L, int k_steps, int N) {
+  const int sms = fwdtiles::sm_count();
+  Plan best{};
+  double cost = 1e300;
+  auto consider = [&](bool few, int rows, int cols, double call, double tile, double step) {
+    const int most = few ? sms : sms / 2;
+    const int64_t tiles = (int64_t)Bt * ceil_div(L, rows) * ceil_div(N, cols);
+    const int whole = (int)std::min<int64_t>(tiles, most);
+    const double c0 = call + (double)((tiles + whole - 1) / whole) * (k_steps * step + tile);
+    if (c0 < cost) {
+      cost = c0;
+      best = Plan{few, cols, rows, whole, false};
+    }
+    // below 16 (6) steps per group the slots cost more than the SMs gained save
+    const int64_t units = tiles * k_steps;
+    const int shared = (int)std::min<int64_t>(most, units / (few ? 6 : 16));
+    if (shared < 2 || tiles > 4 * most || units >= INT32_MAX) return;
+    const double outputs = 1e-6 * Bt * L * N;
+    const double c1 = call + tile + (double)units / shared * step +
+                      (few ? 3.0 + 4.0 * outputs : 6.0 + 6.3 * outputs);
+    if (c1 < cost) {
+      cost = c1;
+      best = Plan{few, cols, rows, shared, true};
+    }
+  };
+  if (L <= 16) consider(true, 16, 128, 5.2, 0.4, 0.195);
+  else if (L <= 32) consider(true, 32, 128, 5.5, 0.4, 0.20);
+  else if (L <= 64) consider(true, 64, 128, 6.2, 0.4, 0.21);
+  else if (L <= 128) consider(true, 128, 128, 8.0, 0.4, 0.224);
+  consider(false, 256, 256, 6.2, 2.6, 0.285);
+  consider(false, 256, 128, 6.0, 1.5, 0.185);
+  consider(false, 256, 64, 6.0, 1.0, 0.165);
+  return best;
 }
 
 }  // namespace linear
 
-size_t linear_workspace(int, int, int, int) { return 0; }
+size_t linear_workspace(int Bt, int L, int K, int N) {
+  const int k_steps = ceil_div(K, linear::kBK);
+  const size_t apart = linear::plan_of(Bt, L, k_steps, N).workspace(L);
+  const size_t merged = linear::plan_of(1, Bt * L, k_steps, N).workspace(Bt * L);
+  return std::max(apart, merged);  // the strides say which; the larger serves both
+}
 
 cudaError_t launch_linear(const LinearArgs& in, cudaStream_t st) {
   LinearArgs a = in;
