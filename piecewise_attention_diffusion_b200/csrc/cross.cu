@@ -55,6 +55,9 @@ struct Params {
   const int32_t* key_len;
   const uint8_t* key_mask;
   float scale_log2;
+  void* o;
+  bsa_strides os;
+  int o32;                   // O's rows lie on whole 32 bytes
   float* lse;
   float* part_o;   // [splits, Bt H Lq, D]
   float2* part_ml; // [splits, Bt H Lq]: running maximum (base 2) and sum
@@ -119,7 +122,7 @@ struct Barriers {
   uint64_t k_full[4], k_empty[4], v_full[4], v_empty[4], v_clear[4];
   uint64_t q_full[kStreams];
   uint64_t s_full[kStreams], p_full[kStreams];
-  uint64_t o_final[kStreams], o_free[kStreams], o_staged[kStreams];
+  uint64_t o_final[kStreams], o_free[kStreams], q_empty[kStreams];
   uint64_t done;
 };
 
@@ -131,9 +134,53 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   return r;
 }
 
+// Row maximum that keeps NaN: three inputs at a time, four chains.
+__device__ __forceinline__ float max3_nan(float a, float b, float c) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+__device__ __forceinline__ float row_max(const uint32_t (&r)[kBK]) {
+  float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+  for (int e = 0; e < kBK; e += 8)
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      m[j] = max3_nan(m[j], __uint_as_float(r[e + 2 * j]), __uint_as_float(r[e + 2 * j + 1]));
+  return max3_nan(max3_nan(m[0], m[1], m[2]), m[3], m[3]);
+}
+
+// Coefficients of the degree-4 polynomial for 2^f on [-1/2, 1/2] of least maximum relative
+// error (3.7e-6), from the Remez fit in exp2_poly_fit.py.
+constexpr float kE0 = 0.9999993f, kE1 = 0.6931218f, kE2 = 0.24024744f, kE3 = 0.05591786f,
+                kE4 = 0.009570102f;
+
+// 2^x for a pair on the FMA pipe, x finite or -inf and <= 8: split as in ex2_poly2, whose
+// degree 3 (7.5e-5) would show in the log-sum-exp. Below -126 the result is 2^-126.
+__device__ __forceinline__ float2 ex2_poly4(float2 x) {
+  constexpr float kShift = 12582912.0f;  // 1.5 * 2^23
+  x.x = fmaxf(x.x, -126.0f);
+  x.y = fmaxf(x.y, -126.0f);
+  const float2 t = add2(x, make_float2(kShift, kShift));
+  const float2 f = sub2(x, sub2(t, make_float2(kShift, kShift)));
+  float2 q = fma2(f, make_float2(kE4, kE4), make_float2(kE3, kE3));
+  q = fma2(q, f, make_float2(kE2, kE2));
+  q = fma2(q, f, make_float2(kE1, kE1));
+  q = fma2(q, f, make_float2(kE0, kE0));
+  return make_float2(__uint_as_float(__float_as_uint(q.x) + (__float_as_uint(t.x) << 23)),
+                     __uint_as_float(__float_as_uint(q.y) + (__float_as_uint(t.y) << 23)));
+}
+
+// Pairs of every 8 whose exponentials go to the FMA pipe, the rest to the special-function
+// unit, which alone would need as long as the products (128 x 128 exponentials at 16 a cycle).
+#ifndef POLY8
+#define POLY8 2
+#endif
+constexpr int kPolyOf8 = POLY8;
+
 // P of one row: 2^(s * scale_log2 - m_ref), to TMEM in pairs of T at p_addr; returns the fp32
 // sum.
-template <typename T>
+template <typename T, int kPoly>
 __device__ __forceinline__ float row_exp(const uint32_t (&r)[kBK], float scale_log2, float m_ref,
                                          uint32_t p_addr) {
   const float2 sc = make_float2(scale_log2, scale_log2), nm = make_float2(-m_ref, -m_ref);
@@ -146,7 +193,7 @@ __device__ __forceinline__ float row_exp(const uint32_t (&r)[kBK], float scale_l
     for (int q = 0; q < 32; ++q) {
       const int e = h * 64 + 2 * q;
       const float2 x = fma2(make_float2(__uint_as_float(r[e]), __uint_as_float(r[e + 1])), sc, nm);
-      const float2 v = make_float2(ex2(x.x), ex2(x.y));
+      const float2 v = q % 8 < kPoly ? ex2_poly4(x) : make_float2(ex2(x.x), ex2(x.y));
       acc[q & 3] = add2(acc[q & 3], v);
       pk[q] = pack2<T>(v.x, v.y);
     }
@@ -166,20 +213,17 @@ __device__ __forceinline__ void tma_load_5d(void* dst, const CUtensorMap* map, u
       : "memory");
 }
 
-__device__ __forceinline__ void tma_store_5d(const CUtensorMap* map, const void* src, int x, int y,
-                                             int z, int w, int v) {
-  asm volatile(
-      "cp.async.bulk.tensor.5d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4, %5, %6}], [%1];"
-      ::"l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(src)), "r"(x), "r"(y), "r"(z), "r"(w),
-      "r"(v)
-      : "memory");
+// 32 bytes, aligned.
+__device__ __forceinline__ void store8(void* dst, const uint32_t* r) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(r[0]),
+               "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
 }
 
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreads, 1)
 k_cross(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
-        const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmO,
-        const __grid_constant__ Params p) {
+        const __grid_constant__ CUtensorMap tmV, const __grid_constant__ Params p) {
   using C = Cfg<D>;
   extern __shared__ unsigned char smem_raw[];
   unsigned char* smem = reinterpret_cast<unsigned char*>(
@@ -199,7 +243,7 @@ k_cross(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtenso
       mbar_init(&bars.p_full[x], 128);
       mbar_init(&bars.o_final[x], 1);
       mbar_init(&bars.o_free[x], 128);
-      mbar_init(&bars.o_staged[x], 128);
+      mbar_init(&bars.q_empty[x], 1);
     }
     for (int i = 0; i < C::NK; ++i) {
       mbar_init(&bars.k_full[i], 1);
@@ -221,7 +265,6 @@ k_cross(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtenso
     prefetch_tensormap(&tmQ);
     prefetch_tensormap(&tmK);
     prefetch_tensormap(&tmV);
-    prefetch_tensormap(&tmO);
   }
   tc_fence_before();
   __syncthreads();
@@ -233,115 +276,155 @@ k_cross(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtenso
   if (warp >= kProducerWarp) {
     setmaxnreg_dec<kRegsControl>();
     if (warp == kProducerWarp) {
-      // ------------------------------------------------ TMA producer: K0, V0, K1, V1, ...
-      if (lane == 0) {
-        uint32_t nk = 0, nv = 0;  // tiles loaded so far
-        bool ok = true;
-        for (int i = blockIdx.x; i < p.n_items && ok; i += gridDim.x) {
-          const Item it = item_of(p, i);
-          const int hk = it.h / p.share;
-          for (int t = 0; t < it.n && ok; ++t) {
-            const int row = (it.t0 + t) * kBK;
-            const int ks = nk % C::NK, vs = nv % C::NV;
-            ok = mbar_wait(&bars.k_empty[ks], ((nk / C::NK) & 1) ^ 1, abort_flag, p.wait_ns);
-            if (!ok) break;
+      // ------------------------------- TMA producer: K0, Q of both streams, V0, K1, V1, ...
+      uint32_t nk = 0;  // tiles loaded so far, of K and of V
+      uint32_t nq[kStreams] = {0, 0};
+      bool ok = true;
+      for (int i = blockIdx.x; i < p.n_items && ok; i += gridDim.x) {
+        const Item it = item_of(p, i);
+        const int hk = it.h / p.share;
+        for (int t = 0; t < it.n && ok; ++t) {
+          const int row = (it.t0 + t) * kBK;
+          const int ks = nk % C::NK, vs = nk % C::NV;
+          ok = mbar_wait_warp(&bars.k_empty[ks], ((nk / C::NK) & 1) ^ 1, abort_flag, p.wait_ns);
+          if (!ok) break;
+          if (elect_one()) {
             mbar_arrive_expect_tx(&bars.k_full[ks], C::SLOT);
             tma_load_5d(sK + ks * C::SLOT, &tmK, &bars.k_full[ks], 0, row, 0, hk * p.kh, it.b * p.kb);
-            ++nk;
-            ok = mbar_wait(&bars.v_empty[vs], ((nv / C::NV) & 1) ^ 1, abort_flag, p.wait_ns);
+          }
+          __syncwarp();
+          // the item's queries, as soon as the last item's last scores are computed
+#pragma unroll
+          for (int x = 0; x < kStreams; ++x) {
+            if (t > 0 || !ok || (x == 1 && !it.two)) break;
+            ok = mbar_wait_warp(&bars.q_empty[x], (nq[x] & 1) ^ 1, abort_flag, p.wait_ns);
             if (!ok) break;
+            if (elect_one()) {
+              mbar_arrive_expect_tx(&bars.q_full[x], C::QBYTES);
+              tma_load_5d(smem + x * C::QBYTES, &tmQ, &bars.q_full[x], 0,
+                          it.qt * 2 * kBQ + x * kBQ, 0, it.h * p.qh, it.b * p.qb);
+            }
+            __syncwarp();
+            ++nq[x];
+          }
+          ok = ok && mbar_wait_warp(&bars.v_empty[vs], ((nk / C::NV) & 1) ^ 1, abort_flag, p.wait_ns);
+          ++nk;
+          if (!ok) break;
+          if (elect_one()) {
             mbar_arrive_expect_tx(&bars.v_full[vs], C::SLOT);
             tma_load_5d(sV + vs * C::SLOT, &tmV, &bars.v_full[vs], 0, row, 0, hk * p.vh, it.b * p.vb);
-            ++nv;
           }
-        }
-        if (!ok) {
-          // drain: wait (bounded, ignoring the abort flag) for copies still in flight
-          const uint64_t t0 = globaltimer_ns();
-          for (uint32_t r = nk > (uint32_t)C::NK ? nk - C::NK : 0; r < nk; ++r)
-            while (!mbar_try_wait(&bars.k_full[r % C::NK], (r / C::NK) & 1) &&
-                   globaltimer_ns() - t0 < 100000000ull) {
-            }
-          for (uint32_t r = nv > (uint32_t)C::NV ? nv - C::NV : 0; r < nv; ++r)
-            while (!mbar_try_wait(&bars.v_full[r % C::NV], (r / C::NV) & 1) &&
-                   globaltimer_ns() - t0 < 100000000ull) {
-            }
+          __syncwarp();
         }
       }
-      __syncwarp();
+      if (!ok) {
+        // drain: wait (bounded, ignoring the abort flag) for copies still in flight
+        const uint64_t t0 = globaltimer_ns();
+        for (uint32_t r = nk > (uint32_t)C::NK ? nk - C::NK : 0; r < nk; ++r)
+          while (!mbar_try_wait(&bars.k_full[r % C::NK], (r / C::NK) & 1) &&
+                 globaltimer_ns() - t0 < 100000000ull) {
+          }
+        for (uint32_t r = nk > (uint32_t)C::NV ? nk - C::NV : 0; r < nk; ++r)
+          while (!mbar_try_wait(&bars.v_full[r % C::NV], (r / C::NV) & 1) &&
+                 globaltimer_ns() - t0 < 100000000ull) {
+          }
+        for (int x = 0; x < kStreams; ++x)
+          while (nq[x] > 0 && !mbar_try_wait(&bars.q_full[x], (nq[x] - 1) & 1) &&
+                 globaltimer_ns() - t0 < 100000000ull) {
+          }
+        __syncwarp();
+      }
     } else if (warp == kMmaWarp) {
       // -------------------------------------------------------------------- MMA issuer
-      if (lane == 0) {
-        constexpr uint32_t fmt = is_bf16<T>() ? 1u : 0u;
-        constexpr uint32_t ab = (1u << 4) | (fmt << 7) | (fmt << 10) | ((uint32_t)(kBQ >> 4) << 24);
-        constexpr uint32_t idesc_s = ab | ((uint32_t)(kBK >> 3) << 17);
-        constexpr uint32_t idesc_o = ab | (1u << 16) | ((uint32_t)(D >> 3) << 17);  // V is MN-major
-        uint32_t nk = 0, nv = 0;  // tiles taken so far
-        int items[kStreams] = {0, 0};
-        uint32_t p_count[kStreams] = {0, 0};
-        bool ok = true;
-        auto issue_s = [&](int x, uint32_t k_addr) {
-          const uint64_t a0 = smem_desc_sw128(smem_u32(smem + x * C::QBYTES), 16, 1024);
-          const uint64_t b0 = smem_desc_sw128(k_addr, 16, 1024);
+      constexpr uint32_t fmt = is_bf16<T>() ? 1u : 0u;
+      constexpr uint32_t ab = (1u << 4) | (fmt << 7) | (fmt << 10) | ((uint32_t)(kBQ >> 4) << 24);
+      constexpr uint32_t idesc_s = ab | ((uint32_t)(kBK >> 3) << 17);
+      constexpr uint32_t idesc_o = ab | (1u << 16) | ((uint32_t)(D >> 3) << 17);  // V is MN-major
+      // a tile's descriptor is its address in 16-byte units in a constant pattern
+      const uint64_t q_desc = smem_desc_sw128(smem_u32(smem), 16, 1024);
+      const uint64_t k_desc = smem_desc_sw128(smem_u32(sK), 16, 1024);
+      const uint64_t v_desc = smem_desc_sw128(smem_u32(sV), kBK * 128, 1024);
+      uint32_t nk = 0, nv = 0;  // tiles taken so far
+      int items[kStreams] = {0, 0};
+      uint32_t p_count[kStreams] = {0, 0};
+      bool ok = true;
+      auto issue_s = [&](int x, uint32_t slot) {  // by the elected lane
+        const uint64_t a0 = q_desc + (uint64_t)(x * (C::QBYTES >> 4));
+        const uint64_t b0 = k_desc + (uint64_t)(slot * (C::SLOT >> 4));
 #pragma unroll
-          for (int k = 0; k < D / 16; ++k) {
-            const uint64_t off = (uint64_t)(((k / 4) * (kBQ * 128) + (k % 4) * 32) >> 4);
-            mma_ss(tmem + C::S_COL(x), a0 + off, b0 + off, idesc_s, k > 0 ? 1u : 0u);
-          }
-          mma_commit(&bars.s_full[x]);
-        };
-        for (int i = blockIdx.x; i < p.n_items && ok; i += gridDim.x) {
-          const Item it = item_of(p, i);
-          const int ns = it.two ? 2 : 1;
-          if (it.n > 0)
-            ok = mbar_wait(&bars.k_full[nk % C::NK], (nk / C::NK) & 1, abort_flag, p.wait_ns);
-          for (int x = 0; x < ns && ok; ++x) {
-            // this item's Q is loaded, and the stream's last epilogue has read S and O
-            ok = mbar_wait(&bars.q_full[x], items[x] & 1, abort_flag, p.wait_ns) &&
-                 (items[x] == 0 ||
-                  mbar_wait(&bars.o_free[x], (items[x] - 1) & 1, abort_flag, p.wait_ns));
-            if (!ok) break;
-            tc_fence_after();
-            if (it.n > 0) issue_s(x, smem_u32(sK + nk % C::NK * C::SLOT));
-            ++items[x];
-          }
+        for (int k = 0; k < D / 16; ++k) {
+          const uint64_t off = (uint64_t)(((k / 4) * (kBQ * 128) + (k % 4) * 32) >> 4);
+          mma_ss(tmem + C::S_COL(x), a0 + off, b0 + off, idesc_s, k > 0 ? 1u : 0u);
+        }
+        mma_commit(&bars.s_full[x]);
+      };
+      for (int i = blockIdx.x; i < p.n_items && ok; i += gridDim.x) {
+        const Item it = item_of(p, i);
+        if (it.n == 0) continue;
+        const int ns = it.two ? 2 : 1;
+        // the first scores: the last item's products, issued before, have taken P from where
+        // these go; its epilogue still reads O
+        ok = mbar_wait_warp(&bars.k_full[nk % C::NK], (nk / C::NK) & 1, abort_flag, p.wait_ns);
+#pragma unroll
+        for (int x = 0; x < kStreams; ++x) {
+          if (x >= ns || !ok) break;
+          ok = mbar_wait_warp(&bars.q_full[x], items[x] & 1, abort_flag, p.wait_ns);
           if (!ok) break;
-          if (it.n > 0) mma_commit(&bars.k_empty[nk++ % C::NK]);
-          for (int t = 0; t < it.n && ok; ++t) {
-            const bool more = t + 1 < it.n;
-            const uint32_t vs = nv % C::NV, ks = nk % C::NK;
-            // V(t), cleared of what is masked where there are masks, and K(t + 1)
-            ok = mbar_wait(&bars.v_full[vs], (nv / C::NV) & 1, abort_flag, p.wait_ns) &&
-                 (!clearing || mbar_wait(&bars.v_clear[vs], (nv / C::NV) & 1, abort_flag, p.wait_ns)) &&
-                 (!more || mbar_wait(&bars.k_full[ks], (nk / C::NK) & 1, abort_flag, p.wait_ns));
-            for (int x = 0; x < ns && ok; ++x) {
-              ok = mbar_wait(&bars.p_full[x], p_count[x] & 1, abort_flag, p.wait_ns);
-              if (!ok) break;
-              ++p_count[x];
-              tc_fence_after();
-              const uint64_t b0 = smem_desc_sw128(smem_u32(sV + vs * C::SLOT), kBK * 128, 1024);
+          tc_fence_after();
+          if (elect_one()) {
+            issue_s(x, nk % C::NK);
+            if (it.n == 1) mma_commit(&bars.q_empty[x]);
+          }
+          __syncwarp();
+          ++items[x];
+        }
+        if (!ok) break;
+        if (elect_one()) mma_commit(&bars.k_empty[nk % C::NK]);
+        __syncwarp();
+        ++nk;
+        for (int t = 0; t < it.n && ok; ++t) {
+          const bool more = t + 1 < it.n;
+          const uint32_t vs = nv % C::NV, ks = nk % C::NK;
+          // V(t), cleared of what is masked where there are masks, and K(t + 1)
+          ok = mbar_wait_warp(&bars.v_full[vs], (nv / C::NV) & 1, abort_flag, p.wait_ns) &&
+               (!clearing ||
+                mbar_wait_warp(&bars.v_clear[vs], (nv / C::NV) & 1, abort_flag, p.wait_ns)) &&
+               (!more || mbar_wait_warp(&bars.k_full[ks], (nk / C::NK) & 1, abort_flag, p.wait_ns));
+#pragma unroll
+          for (int x = 0; x < kStreams; ++x) {
+            if (x >= ns || !ok) break;
+            ok = mbar_wait_warp(&bars.p_full[x], p_count[x] & 1, abort_flag, p.wait_ns) &&
+                 (t > 0 || items[x] == 1 ||  // the stream's last epilogue has read O
+                  mbar_wait_warp(&bars.o_free[x], (items[x] - 2) & 1, abort_flag, p.wait_ns));
+            if (!ok) break;
+            ++p_count[x];
+            tc_fence_after();
+            if (elect_one()) {
+              const uint64_t b0 = v_desc + (uint64_t)(vs * (C::SLOT >> 4));
 #pragma unroll
               for (int k = 0; k < kBK / 16; ++k)
                 mma_ts(tmem + C::O_COL(x), tmem + C::S_COL(x) + k * 8, b0 + (uint64_t)(k * 128),
-                       idesc_o, (t | k) ? 1u : 0u);
-              if (more) issue_s(x, smem_u32(sK + ks * C::SLOT));
+                       idesc_o, t > 0 || k > 0 ? 1u : 0u);
+              if (more) issue_s(x, ks);
+              else mma_commit(&bars.o_final[x]);
+              if (t + 2 == it.n) mma_commit(&bars.q_empty[x]);
             }
-            if (!ok) break;
-            mma_commit(&bars.v_empty[vs]);
-            ++nv;
-            if (more) {
-              mma_commit(&bars.k_empty[ks]);
-              ++nk;
-            }
+            __syncwarp();
           }
           if (!ok) break;
-          for (int x = 0; x < ns; ++x) mma_commit(&bars.o_final[x]);
+          if (elect_one()) {
+            mma_commit(&bars.v_empty[vs]);
+            if (more) mma_commit(&bars.k_empty[ks]);
+          }
+          __syncwarp();
+          ++nv;
+          nk += more;
         }
-        // every issued MMA must complete before TMEM is released
-        mma_commit(&bars.done);
-        const uint64_t t0 = globaltimer_ns();
-        while (!mbar_try_wait(&bars.done, 0) && globaltimer_ns() - t0 < 100000000ull) {
-        }
+      }
+      // every issued MMA must complete before TMEM is released
+      if (elect_one()) mma_commit(&bars.done);
+      const uint64_t t0 = globaltimer_ns();
+      while (!mbar_try_wait(&bars.done, 0) && globaltimer_ns() - t0 < 100000000ull) {
       }
       __syncwarp();
     } else if (warp == kClearWarp) {
@@ -387,33 +470,14 @@ k_cross(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtenso
     // keys up to 2^-31 below the row's largest still count
     constexpr float kLift = is_bf16<T>() ? 0.f : 7.f;
     const int x = warp / 4, quad = warp % 4, row = quad * 32 + lane;
-    const bool leader = quad == 0 && lane == 0;
     const uint32_t lane_addr = (uint32_t)(quad * 32) << 16;
     const uint32_t s_base = tmem + lane_addr + C::S_COL(x);
     const uint32_t o_base = tmem + lane_addr + C::O_COL(x);
-    unsigned char* sq = smem + x * C::QBYTES;
-    // the next item from `from` on that has rows for this stream
-    auto next_item = [&](int from) -> int {
-      for (int i = from; i < p.n_items; i += gridDim.x)
-        if (x == 0 || (i / p.splits % p.q_tiles) * 2 * kBQ + kBQ < p.Lq) return i;
-      return p.n_items;
-    };
-    auto load_q = [&](int i) {
-      const Item it = item_of(p, i);
-      mbar_arrive_expect_tx(&bars.q_full[x], C::QBYTES);
-      tma_load_5d(sq, &tmQ, &bars.q_full[x], 0, it.qt * 2 * kBQ + x * kBQ, 0, it.h * p.qh, it.b * p.qb);
-    };
-    int q_issued = 0;
-    int i = next_item(blockIdx.x);
-    if (leader && i < p.n_items) {
-      load_q(i);
-      ++q_issued;
-    }
-    uint32_t tiles = 0;
+    uint32_t tiles = 0, finals = 0;
     bool ok = true;
-    for (int k = 0; i < p.n_items && ok; ++k) {
+    for (int i = blockIdx.x; i < p.n_items; i += gridDim.x) {
       const Item it = item_of(p, i);
-      const int following = next_item(i + gridDim.x);
+      if (x == 1 && !it.two) continue;
       const int row_g = it.qt * 2 * kBQ + x * kBQ + row;
       float m_run = -INFINITY, l = 0.f;
       for (int t = 0; t < it.n; ++t) {
@@ -436,7 +500,7 @@ k_cross(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtenso
           for (int e = 0; e < kBK; ++e)
             if ((excl[e >> 5] >> (e & 31)) & 1u) r[e] = __float_as_uint(-INFINITY);
         }
-        const float mx = fwdtiles::row_max<kBK, kBK>(r) * p.scale_log2;
+        const float mx = row_max(r) * p.scale_log2;
         const bool need = mx > m_run + kRescaleLog2;
         if (__any_sync(0xffffffffu, need)) {
           const float m_new = need ? mx : m_run;
@@ -457,7 +521,11 @@ k_cross(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtenso
           m_run = m_new;
         }
         const float m_ref = m_run == -INFINITY ? 0.f : m_run - kLift;
-        l += row_exp<T>(r, p.scale_log2, m_ref, s_base);
+        // NaN and +inf only come out right on the special-function unit
+        if (__any_sync(0xffffffffu, !(mx < INFINITY)))
+          l += row_exp<T, 0>(r, p.scale_log2, m_ref, s_base);
+        else
+          l += row_exp<T, kPolyOf8>(r, p.scale_log2, m_ref, s_base);
         tmem_wait_st();
         tc_fence_before();
         mbar_arrive(&bars.p_full[x]);
@@ -465,85 +533,64 @@ k_cross(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtenso
       if (!ok) break;
 
       // ------------------------------------------------------------------ epilogue
-      ok = mbar_wait(&bars.o_final[x], k & 1, abort_flag, p.wait_ns);
-      ok = __all_sync(0xffffffffu, ok);
-      if (!ok) break;
-      tc_fence_after();
+      if (it.n > 0) {
+        ok = mbar_wait(&bars.o_final[x], finals & 1, abort_flag, p.wait_ns);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        ++finals;
+        tc_fence_after();
+      }
       const bool write = row_g < p.Lq;
       const int64_t row_of = ((int64_t)it.b * p.H + it.h) * p.Lq + row_g;
-      // a row without a real key has l = 0 and outputs zeros; NaN stays NaN
+      // a row without a real key outputs zeros (its l is what the polynomial makes of -inf);
+      // NaN stays NaN
+      if (m_run == -INFINITY && l < 1.f) l = 0.f;
       const float inv_l = l == 0.f ? 0.f : 1.0f / l;
       if (p.splits > 1) {
         const int64_t at = (int64_t)it.split * p.Bt * p.H * p.Lq + row_of;
         if (write) p.part_ml[at] = make_float2(m_run - kLift, l);
 #pragma unroll 1
-        for (int c = 0; c < D && it.n > 0; c += 16) {
-          uint32_t ro[16];
-          tmem_ld16(o_base + c, ro);
+        for (int c = 0; c < D && it.n > 0; c += 32) {
+          uint32_t ro[32];
+          tmem_ld32(o_base + c, ro);
           tmem_wait_ld();
-          if (write) {
-            uint4* dst = reinterpret_cast<uint4*>(p.part_o + at * D + c);
+          if (write)
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-              dst[e] = make_uint4(ro[4 * e], ro[4 * e + 1], ro[4 * e + 2], ro[4 * e + 3]);
-          }
-        }
-        if (leader && following < p.n_items) {
-          load_q(following);
-          ++q_issued;
+            for (int e = 0; e < 32; e += 8) store8(p.part_o + at * D + c + e, ro + e);
         }
       } else {
+        // the rows leave from registers, 32 bytes a lane: no staging, so that Q's tile is free
+        // for the next item long before
+        T* o = static_cast<T*>(p.o) + it.b * p.os.batch + it.h * p.os.head + row_g * p.os.row;
 #pragma unroll 1
-        for (int c = 0; c < D; c += 16) {
-          uint32_t ro[16];
+        for (int c = 0; c < D; c += 32) {
+          uint32_t ro[32] = {}, packed[16];
           if (it.n > 0) {
-            tmem_ld16(o_base + c, ro);
+            tmem_ld32(o_base + c, ro);
             tmem_wait_ld();
           }
-          uint32_t packed[8];
 #pragma unroll
-          for (int e = 0; e < 16; e += 2)
-            packed[e / 2] = it.n > 0 ? pack2<T>(__uint_as_float(ro[e]) * inv_l,
-                                                __uint_as_float(ro[e + 1]) * inv_l)
-                                     : 0u;
-          // Q's tile is free: it stages the output in the same 128-byte swizzle
-          const int j = (c % 64) / 8;
-          unsigned char* dst = sq + (c / 64) * (kBQ * 128) + row * 128;
-          *reinterpret_cast<uint4*>(dst + ((j ^ (row & 7)) * 16)) =
-              make_uint4(packed[0], packed[1], packed[2], packed[3]);
-          *reinterpret_cast<uint4*>(dst + (((j + 1) ^ (row & 7)) * 16)) =
-              make_uint4(packed[4], packed[5], packed[6], packed[7]);
-        }
-        fence_proxy_async_smem();
-        mbar_arrive(&bars.o_staged[x]);
-        bool staged = true;
-        if (leader) {
-          staged = mbar_wait(&bars.o_staged[x], k & 1, abort_flag, p.wait_ns);
-          if (staged) {
-            tma_store_5d(&tmO, sq, 0, it.qt * 2 * kBQ + x * kBQ, 0, it.h, it.b);
-            bulk_commit_group();
-            bulk_wait_read_all();
-            if (following < p.n_items) {
-              load_q(following);
-              ++q_issued;
+          for (int e = 0; e < 16; ++e)
+            packed[e] = pack2<T>(__uint_as_float(ro[2 * e]) * inv_l,
+                                 __uint_as_float(ro[2 * e + 1]) * inv_l);
+          if (write) {
+            if (p.o32) {
+              store8(o + c, packed);
+              store8(o + c + 16, packed + 8);
+            } else {
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                *reinterpret_cast<uint4*>(o + c + 8 * e) = make_uint4(
+                    packed[4 * e], packed[4 * e + 1], packed[4 * e + 2], packed[4 * e + 3]);
             }
           }
         }
-        ok = __all_sync(0xffffffffu, staged);
-        if (!ok) break;
         if (write && p.lse != nullptr)
           p.lse[row_of] = l == 0.f ? -INFINITY : (m_run - kLift + log2f(l)) * 0.69314718055994531f;
       }
-      tc_fence_before();
-      mbar_arrive(&bars.o_free[x]);
-      i = following;
-    }
-    if (leader) bulk_wait_all();
-    if (!ok && leader && q_issued > 0) {
-      // drain this stream's last Q copy (bounded) before the CTA exits
-      const uint64_t t0 = globaltimer_ns();
-      while (!mbar_try_wait(&bars.q_full[x], (q_issued - 1) & 1) &&
-             globaltimer_ns() - t0 < 100000000ull) {
+      if (it.n > 0) {
+        tc_fence_before();
+        mbar_arrive(&bars.o_free[x]);
       }
     }
   }
@@ -652,9 +699,12 @@ cudaError_t run(const CrossArgs& a, cudaStream_t st) {
   p.part_o = static_cast<float*>(a.ws) + (p.splits * rows * 2 + 3) / 4 * 4;
   p.status = a.status;
   p.wait_ns = kWaitTimeoutNs;
-  CUtensorMap tmQ, tmK, tmV, tmO;
-  bool ok = map_5d<T>(&tmQ, a.Q, D, a.Lq, a.H, a.Bt, a.qs) &&
-            map_5d<T>(&tmO, a.O, D, a.Lq, a.H, a.Bt, a.os);
+  p.o = a.O;
+  p.os = a.os;
+  p.o32 = (reinterpret_cast<uintptr_t>(a.O) & 31u) == 0 && a.os.batch % 16 == 0 &&
+          a.os.head % 16 == 0 && a.os.row % 16 == 0;
+  CUtensorMap tmQ, tmK, tmV;
+  bool ok = map_5d<T>(&tmQ, a.Q, D, a.Lq, a.H, a.Bt, a.qs);
   if (a.Lk > 0)
     ok = ok && map_5d<T>(&tmK, a.K, D, a.Lk, a.Hkv, a.Bt, a.ks) &&
          map_5d<T>(&tmV, a.V, D, a.Lk, a.Hkv, a.Bt, a.vs);
@@ -669,8 +719,7 @@ cudaError_t run(const CrossArgs& a, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   if (fa.numRegs * kThreads < 128 * kRegsControl + 256 * kRegsSoftmax)
     return cudaErrorInvalidConfiguration;
-  k_cross<T, D><<<std::min(p.n_items, fwdtiles::sm_count()), kThreads, C::SMEM, st>>>(tmQ, tmK, tmV,
-                                                                                      tmO, p);
+  k_cross<T, D><<<std::min(p.n_items, fwdtiles::sm_count()), kThreads, C::SMEM, st>>>(tmQ, tmK, tmV, p);
   e = cudaGetLastError();
   if (e != cudaSuccess || p.splits == 1) return e;
   k_join<T, D><<<(unsigned)((rows + 3) / 4), 128, 0, st>>>(p, static_cast<T*>(a.O), a.os);
