@@ -77,6 +77,13 @@ cudaError_t launch_forward_tc(const ForwardArgs& a, const int32_t* flag, cudaStr
 cudaError_t launch_forward_pair(const ForwardArgs& a, const int32_t* flag, const void* kb16,
                                 const void* vs16, const void* hb16, int Mp, cudaStream_t st);
 
+// The first 32-byte boundary of a workspace: callers give 16-byte aligned ones, the kernels'
+// 32-byte stores want more. Sizes count kAlignSlack for it.
+constexpr size_t kAlignSlack = 16;
+inline float* align32(void* ws) {
+  return reinterpret_cast<float*>((reinterpret_cast<uintptr_t>(ws) + 31) & ~uintptr_t(31));
+}
+
 struct RotaryArgs {
   const void* X;
   bsa_strides xs;

@@ -173,7 +173,7 @@ struct Plan {
   int groups;
   bool split;
   size_t workspace(int L) const {
-    return split ? (size_t)2 * groups * std::min(L, rows) * cols * sizeof(float) : 0;
+    return split ? (size_t)2 * groups * std::min(L, rows) * cols * sizeof(float) + kAlignSlack : 0;
   }
 };
 Plan plan_of(int Bt, int L, int k_steps, int N);
@@ -203,7 +203,7 @@ Params<T> params_of(const LinearArgs& a, const Plan& plan) {
   p.yv = View{a.ys.batch, a.ys.head, a.ys.row, dy};
   p.tma_out = whole16(a.Y, a.ys);
   p.vec_res = a.R != nullptr && a.N % 8 == 0 && whole16(a.R, a.rs);
-  p.part = static_cast<float*>(a.ws);
+  p.part = align32(a.ws);
   p.part_rows = std::min(a.L, plan.rows);
   p.status = a.status;
   p.wait_ns = kWaitTimeoutNs;

@@ -183,6 +183,21 @@ def test_strided_views_and_what_lies_beside_them(Lq, Lk):
     _check(o, lse, q, k1, v1)
 
 
+@pytest.mark.parametrize("d,Lk", [(64, 2000), (128, 3001)])
+def test_workspace_at_any_16_byte_boundary_and_outputs_too(d, Lk):
+    q, k, v = _randn(1, 3, 1, d), _randn(1, 3, Lk, d, seed=1), _randn(1, 3, Lk, d, seed=2)
+    need = b.bsa_cross_workspace_bytes(1, 3, 3, 1, Lk, d)
+    assert need > 0
+    for off in (0, 16, 32, 48):
+        ws = torch.full((need + 64,), 255, dtype=torch.uint8, device=DEV)
+        buf = torch.full((3 * d + 64,), 6.0, dtype=torch.bfloat16, device=DEV)
+        out = buf[off // 2:off // 2 + 3 * d].view(1, 3, 1, d)
+        o, lse = b.cross_forward(q, k, v, ws=ws[off:off + need], out=out, want_lse=True)
+        _check(o, lse, q, k, v)
+        assert (ws[:off] == 255).all() and (ws[off + need:] == 255).all()
+        assert (buf[:off // 2] == 6).all() and (buf[off // 2 + 3 * d:] == 6).all()
+
+
 @pytest.mark.parametrize("Lq,Lk", [(150, 260), (3, 1300)])
 def test_scores_at_their_ends(Lq, Lk):
     """Scores in the thousands of either sign, rows that grow from tile to tile, and rows that

@@ -189,6 +189,19 @@ def test_same_bits_every_time_other_streams_and_a_replayed_graph():
         assert torch.equal(out, b.linear(x, w, bias))
 
 
+@pytest.mark.parametrize("L,K,N", [(2, 8192, 256), (300, 16384, 128)])
+def test_workspace_at_any_16_byte_boundary(L, K, N):
+    x, w = _randn(1, L, K), _randn(N, K, seed=1, scale=K ** -0.5)
+    need = b.bsa_linear_workspace_bytes(1, L, K, N)
+    assert need > 0
+    want = b.linear(x, w)
+    _check(want, x, w)
+    for off in (16, 32, 48):
+        ws = torch.full((need + 64,), 255, dtype=torch.uint8, device=DEV)
+        assert torch.equal(b.linear(x, w, ws=ws[off:off + need]), want)
+        assert (ws[:off] == 255).all() and (ws[off + need:] == 255).all()
+
+
 def test_more_than_2_31_outputs():
     """Offsets past 32 bits: rows at the end of an output of 2^31 + elements."""
     N = 4096
