@@ -320,7 +320,7 @@ bsa_status bsa_linear(const void* X, const bsa_strides* xs, int32_t x_heads, con
 size_t bsa_cross_workspace_bytes(int32_t Bt, int32_t H, int32_t Hkv, int32_t Lq, int32_t Lk,
                                  int32_t d) {
   if (check_cross(Bt, H, Hkv, Lq, Lk, d) != BSA_OK) return 0;
-  return bsa::cross_workspace(Bt, H, Lq, Lk, d);
+  return bsa::cross_workspace(Bt, H, Hkv, Lq, Lk, d);
 }
 
 bsa_status bsa_cross_forward(const void* Q, const bsa_strides* qs, const void* K,
@@ -353,7 +353,7 @@ bsa_status bsa_cross_forward(const void* Q, const bsa_strides* qs, const void* K
   if ((Lq > 1 && (a.qs.row == 0 || a.os.row == 0)) || (Lk > 1 && (a.ks.row == 0 || a.vs.row == 0)))
     return BSA_ERR_INVALID_ARG;
   if ((Bt > 1 && a.os.batch == 0) || (H > 1 && a.os.head == 0)) return BSA_ERR_INVALID_ARG;
-  if (!workspace_ok(bsa::cross_workspace(Bt, H, Lq, Lk, d), workspace, ws_bytes))
+  if (!workspace_ok(bsa::cross_workspace(Bt, H, Hkv, Lq, Lk, d), workspace, ws_bytes))
     return BSA_ERR_WORKSPACE;
   return from_cuda(bsa::launch_cross(a, static_cast<cudaStream_t>(stream)));
 }

@@ -241,6 +241,8 @@ k_cross(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtenso
   __shared__ uint32_t tmem_base_sh;
   __shared__ int abort_sh;
 
+  // k_join may take its place now; it waits for this grid before it reads a run
+  if (p.splits > 1) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   if (threadIdx.x == 0) {
     abort_sh = 0;
@@ -614,40 +616,53 @@ k_cross(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtenso
   }
 }
 
-// The runs of one row, joined in order: m = max m_i, o = sum 2^(m_i - m) o_i / l with
-// l = sum 2^(m_i - m) l_i. One warp per row.
+// The runs of one row, joined in a fixed order: m = max m_i, o = sum 2^(m_i - m) o_i / l with
+// l = sum 2^(m_i - m) l_i. One warp per row; its lanes take the runs' m and l, 32 at a time.
 template <typename T, int D>
 __global__ void __launch_bounds__(128)
-k_join(const Params p, T* o, bsa_strides os) {
-  const int64_t rows = (int64_t)p.Bt * p.H * p.Lq;
+k_join(const float* part_o, const float2* part_ml, int splits, int64_t rows, int H, int Lq, T* o,
+       bsa_strides os, float* lse) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const int64_t row = (int64_t)blockIdx.x * 4 + threadIdx.x / 32;
   const int lane = threadIdx.x % 32;
   if (row >= rows) return;
   float m = -INFINITY;
-  for (int s = 0; s < p.splits; ++s) {
-    const float2 ml = p.part_ml[s * rows + row];
+  for (int s = lane; s < splits; s += 32) {
+    const float2 ml = part_ml[s * rows + row];
     if (ml.y != 0.f) m = fmaxf(m, ml.x);
   }
+  m = warp_max(m);
   constexpr int V = D / 32;
   float acc[V] = {}, l = 0.f;
-  for (int s = 0; s < p.splits; ++s) {
-    const float2 ml = p.part_ml[s * rows + row];
-    if (ml.y == 0.f) continue;  // no real key in this run: its O was not written
-    const float w = exp2f(ml.x - m);
-    l += w * ml.y;
-    const Pack<float, V> part =
-        *reinterpret_cast<const Pack<float, V>*>(p.part_o + (s * rows + row) * D + lane * V);
+  for (int s0 = 0; s0 < splits; s0 += 32) {
+    float w = 0.f;
+    if (s0 + lane < splits) {
+      const float2 ml = part_ml[(s0 + lane) * rows + row];
+      if (ml.y != 0.f) {
+        w = exp2f(ml.x - m);
+        l += w * ml.y;
+      }
+    }
+    const int n = min(32, splits - s0);
+#pragma unroll 4
+    for (int s = 0; s < n; ++s) {
+      const float ws = __shfl_sync(0xffffffffu, w, s);
+      if (ws == 0.f) continue;  // no real key in this run: its O was not written
+      const Pack<float, V> part = *reinterpret_cast<const Pack<float, V>*>(
+          part_o + ((s0 + s) * rows + row) * D + lane * V);
 #pragma unroll
-    for (int e = 0; e < V; ++e) acc[e] += w * part.v[e];
+      for (int e = 0; e < V; ++e) acc[e] += ws * part.v[e];
+    }
   }
+  l = warp_sum(l);
   const float inv = l == 0.f ? 0.f : 1.0f / l;
   Pack<T, V> out;
 #pragma unroll
   for (int e = 0; e < V; ++e) out.v[e] = from_f32<T>(acc[e] * inv);
-  const int t = (int)(row % p.Lq), h = (int)(row / p.Lq % p.H), b = (int)(row / p.Lq / p.H);
+  const int t = (int)(row % Lq), h = (int)(row / Lq % H), b = (int)(row / Lq / H);
   *reinterpret_cast<Pack<T, V>*>(o + b * os.batch + h * os.head + t * os.row + lane * V) = out;
-  if (lane == 0 && p.lse != nullptr)
-    p.lse[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
+  if (lane == 0 && lse != nullptr)
+    lse[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
 }
 
 // ------------------------------------------------------------------ host side
@@ -671,21 +686,66 @@ bool map_5d(CUtensorMap* m, const void* ptr, int D, int L, int H, int Bt, const 
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Runs of key tiles per row tile: as many as fill the SMs, none below four tiles.
-int splits_of(int Bt, int H, int Lq, int Lk) {
+// How a call is run: by k_cross_few or k_cross, and in how many runs of keys.
+struct Plan {
+  bool few;
+  int splits;
+};
+Plan plan_of(int Bt, int H, int Hkv, int Lq, int Lk) {
+  const int sms = fwdtiles::sm_count();
+  if (Lk > 0 && (int64_t)H / Hkv * Lq <= kMostRows && Bt <= 65535 && Hkv <= 65535) {
+    // the runs per head that leave least of the last wave of CTAs empty, 256 keys each at least
+    const int64_t heads = (int64_t)Bt * Hkv, wave = (int64_t)kFewPerSm * sms;
+    const int most = (int)std::min<int64_t>(std::max<int64_t>(1, 2 * wave / heads),
+                                            std::max(1, Lk / 256));
+    Plan best{true, 1};
+    double cost = 1e300;
+    for (int s = 1; s <= most; ++s) {
+      const double c = (double)((heads * s + wave - 1) / wave) / s + 1e-4 * s;
+      if (c < cost) {
+        cost = c;
+        best.splits = s;
+      }
+    }
+    return best;
+  }
+  // runs of key tiles per row tile: as many as fill the SMs, none below four tiles
   const int64_t items = (int64_t)Bt * H * ceil_div(Lq, 2 * kBQ);
   const int tiles = ceil_div(Lk, kBK);
-  const int64_t want = fwdtiles::sm_count() / items;
-  if (want < 2) return 1;
-  const int most = std::max(1, tiles / 4);
-  int splits = (int)std::min<int64_t>(want, most);
-  const int per = ceil_div(tiles, splits);
-  return ceil_div(tiles, per);
+  const int64_t want = sms / items;
+  if (want < 2 || tiles < 8) return Plan{false, 1};
+  const int per = ceil_div(tiles, (int)std::min<int64_t>(want, tiles / 4));
+  return Plan{false, ceil_div(tiles, per)};
+}
+
+template <typename T, int D>
+cudaError_t join(const CrossArgs& a, int splits, const float* part_o, const float2* part_ml,
+                 cudaStream_t st) {
+  const int64_t rows = (int64_t)a.Bt * a.H * a.Lq;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)((rows + 3) / 4));
+  cfg.blockDim = dim3(128);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, k_join<T, D>, part_o, part_ml, splits, rows, a.H, a.Lq,
+                            static_cast<T*>(a.O), a.os, a.lse);
 }
 
 template <typename T, int D>
 cudaError_t run(const CrossArgs& a, cudaStream_t st) {
   using C = Cfg<D>;
+  const Plan plan = plan_of(a.Bt, a.H, a.Hkv, a.Lq, a.Lk);
+  const int64_t rows = (int64_t)a.Bt * a.H * a.Lq;
+  float* part_o = align32(a.ws);
+  float2* part_ml = reinterpret_cast<float2*>(part_o + plan.splits * rows * D);
+  if (plan.few) {
+    const cudaError_t e = run_few(a, plan.splits, part_o, part_ml, st);
+    return e != cudaSuccess ? e : join<T, D>(a, plan.splits, part_o, part_ml, st);
+  }
   Params p;
   p.Bt = a.Bt;
   p.H = a.H;
@@ -693,7 +753,7 @@ cudaError_t run(const CrossArgs& a, cudaStream_t st) {
   p.Lq = a.Lq;
   p.Lk = a.Lk;
   p.q_tiles = ceil_div(a.Lq, 2 * kBQ);
-  p.splits = a.Lk > 0 ? splits_of(a.Bt, a.H, a.Lq, a.Lk) : 1;
+  p.splits = plan.splits;
   p.tiles_per_split = ceil_div(std::max(ceil_div(a.Lk, kBK), 1), p.splits);
   p.n_items = a.Bt * a.H * p.q_tiles * p.splits;
   p.qb = a.qs.batch != 0;
@@ -706,9 +766,8 @@ cudaError_t run(const CrossArgs& a, cudaStream_t st) {
   p.key_mask = a.key_mask;
   p.scale_log2 = a.scale * 1.4426950408889634f;
   p.lse = a.lse;
-  const int64_t rows = (int64_t)a.Bt * a.H * a.Lq;
-  p.part_o = align32(a.ws);
-  p.part_ml = reinterpret_cast<float2*>(p.part_o + p.splits * rows * D);
+  p.part_o = part_o;
+  p.part_ml = part_ml;
   p.status = a.status;
   p.wait_ns = kWaitTimeoutNs;
   CUtensorMap tmQ, tmK, tmV, tmO;
@@ -732,18 +791,16 @@ cudaError_t run(const CrossArgs& a, cudaStream_t st) {
       tmQ, tmK, tmV, tmO, p);
   e = cudaGetLastError();
   if (e != cudaSuccess || p.splits == 1) return e;
-  k_join<T, D><<<(unsigned)((rows + 3) / 4), 128, 0, st>>>(p, static_cast<T*>(a.O), a.os);
-  return cudaGetLastError();
+  return join<T, D>(a, p.splits, part_o, part_ml, st);
 }
 
 }  // namespace cross
 
-size_t cross_workspace(int Bt, int H, int Lq, int Lk, int d) {
-  if (Lk <= 0) return 0;
-  const int splits = cross::splits_of(Bt, H, Lq, Lk);
-  if (splits == 1) return 0;
+size_t cross_workspace(int Bt, int H, int Hkv, int Lq, int Lk, int d) {
+  const cross::Plan plan = cross::plan_of(Bt, H, Hkv, Lq, Lk);
+  if (!plan.few && plan.splits == 1) return 0;
   const size_t rows = (size_t)Bt * H * Lq;
-  return splits * rows * (d + 2) * sizeof(float) + kAlignSlack;
+  return plan.splits * rows * (d + 2) * sizeof(float) + kAlignSlack;
 }
 
 cudaError_t launch_cross(const CrossArgs& a, cudaStream_t st) {

@@ -136,7 +136,14 @@ struct CrossArgs {
   void* ws;
   int32_t* status;
 };
-size_t cross_workspace(int Bt, int H, int Lq, int Lk, int d);
+namespace cross {
+// The kernel for few query rows (cross_few.cu): a key head's query heads times Lq at most
+// kMostRows; kFewPerSm CTAs share an SM. Leaves `splits` parts per row for k_join.
+constexpr int kMostRows = 4, kFewPerSm = 2;
+cudaError_t run_few(const CrossArgs& a, int splits, float* part_o, float2* part_ml,
+                    cudaStream_t st);
+}  // namespace cross
+size_t cross_workspace(int Bt, int H, int Hkv, int Lq, int Lk, int d);
 cudaError_t launch_cross(const CrossArgs& a, cudaStream_t st);
 
 }  // namespace bsa
