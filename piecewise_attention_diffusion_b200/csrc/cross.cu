@@ -126,14 +126,6 @@ struct Barriers {
   uint64_t done;
 };
 
-template <typename T>
-__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
-  if (is_bf16<T>()) return pack_bf16x2(lo, hi);
-  uint32_t r;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-
 // Row maximum that keeps NaN: three inputs at a time, four chains.
 __device__ __forceinline__ float max3_nan(float a, float b, float c) {
   float d;

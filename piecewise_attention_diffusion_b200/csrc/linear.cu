@@ -237,17 +237,16 @@ k_linear(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtens
       // lane, and 32 columns of the row's residual; asked for a chunk ahead
       struct Ahead {
         T bias, gate;
-        Pack<T, 8> res[kCW / 8];
+        uint4 res[kCW / 8];
       } ahead;
       auto fetch = [&](int col0) {
         const bool in = col0 + lane < p.N;
         ahead.bias = in && p.bias != nullptr ? p.bias[col0 + lane] : from_f32<T>(0.f);
         ahead.gate = in && p.gate != nullptr && one_gate ? gate[col0 + lane] : from_f32<T>(1.f);
       };
-      auto fetch_res = [&](int col) -> Pack<T, 8> {
+      auto fetch_res = [&](int col) -> uint4 {
         const int head = col / p.rv.cols;
-        return *reinterpret_cast<const Pack<T, 8>*>(res_row + head * p.rv.head +
-                                                    (col - head * p.rv.cols));
+        return *reinterpret_cast<const uint4*>(res_row + head * p.rv.head + (col - head * p.rv.cols));
       };
       const bool vec_res = p.vec_res && live;  // then 8 columns are all there or all not
       const bool rows_here = row0 < p.L;
@@ -311,8 +310,8 @@ k_linear(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtens
           const int col = col0 + g * 8;
           // the 64-byte swizzle of the store's box: 16-byte piece g of row r sits at
           // g ^ (r / 2 % 4)
-          Pack<T, 8>* slot = reinterpret_cast<Pack<T, 8>*>(out + lane * kCW * 2 +
-                                                           (g ^ ((lane >> 1) & 3)) * 16);
+          uint4* slot =
+              reinterpret_cast<uint4*>(out + lane * kCW * 2 + (g ^ ((lane >> 1) & 3)) * 16);
           float2 v[4];
 #pragma unroll
           for (int i = 0; i < 4; ++i)
@@ -332,19 +331,14 @@ k_linear(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtens
             }
           }
           if (p.res != nullptr) {
-            const Pack<T, 8> w = p.vec_res ? ahead.res[g] : *slot;
+            const uint4 w = p.vec_res ? ahead.res[g] : *slot;
+            const uint32_t words[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-              v[i] = add2(v[i], make_float2(to_f32(w.v[2 * i]), to_f32(w.v[2 * i + 1])));
+            for (int i = 0; i < 4; ++i) v[i] = add2(v[i], unpack2<T>(words[i]));
             if (more && vec_res && col + kCW < p.N) ahead.res[g] = fetch_res(col + kCW);
           }
-          Pack<T, 8> o;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            o.v[2 * i] = from_f32<T>(v[i].x);
-            o.v[2 * i + 1] = from_f32<T>(v[i].y);
-          }
-          *slot = o;
+          *slot = make_uint4(pack2<T>(v[0].x, v[0].y), pack2<T>(v[1].x, v[1].y),
+                             pack2<T>(v[2].x, v[2].y), pack2<T>(v[3].x, v[3].y));
         }
         const int yhead = col0 / p.yv.cols, yc = col0 - yhead * p.yv.cols;
         if (p.tma_out) {

@@ -41,6 +41,41 @@ struct Params {
   uint8_t axis[kMaxPairs], lo[kMaxPairs], hi[kMaxPairs];
 };
 
+// N bytes, as words where there are any.
+template <int N>
+struct alignas(N < 16 ? N : 16) Bytes {
+  uint32_t w[N / 4];
+};
+template <>
+struct alignas(2) Bytes<2> {
+  uint16_t w[1];
+};
+
+// Element i of a run of T.
+template <typename T, int N>
+__device__ __forceinline__ float element(const Bytes<N>& b, int i) {
+  if constexpr (N == 2) return to_f32(*reinterpret_cast<const T*>(&b.w[0]));
+  else if constexpr (sizeof(T) == 4) return __uint_as_float(b.w[i]);
+  else return i % 2 == 0 ? unpack2<T>(b.w[i / 2]).x : unpack2<T>(b.w[i / 2]).y;
+}
+
+// A run of T from fp32 values.
+template <typename T, int N>
+__device__ __forceinline__ Bytes<N> run_of(const float (&f)[N / sizeof(T)]) {
+  Bytes<N> b;
+  if constexpr (N == 2) {
+    const T t = from_f32<T>(f[0]);
+    b.w[0] = *reinterpret_cast<const uint16_t*>(&t);
+  } else {
+#pragma unroll
+    for (int i = 0; i < N / 4; ++i) {
+      if constexpr (sizeof(T) == 4) b.w[i] = __float_as_uint(f[i]);
+      else b.w[i] = pack2<T>(f[2 * i], f[2 * i + 1]);
+    }
+  }
+  return b;
+}
+
 // W pairs per thread. kAdjacent: 2W consecutive components; else W consecutive first
 // components and W consecutive second ones (the host chose W so that neither run crosses
 // a section).
@@ -83,50 +118,51 @@ k_rotary(const __grid_constant__ Params p) {
   const int h1 = min(h0 + p.heads_per_cta, p.H);
   const T* x = static_cast<const T*>(p.x) + b * p.xs.batch + t * p.xs.row + h0 * p.xs.head;
   T* y = static_cast<T*>(p.y) + b * p.ys.batch + t * p.ys.row + h0 * p.ys.head;
+  constexpr int kRun = (int)sizeof(T) * W * (kAdjacent ? 2 : 1);
 
   for (int h = h0; h < h1; h += kUnroll) {
-    Pack<T, W> first[kUnroll], second[kUnroll];
+    Bytes<kRun> first[kUnroll], second[kUnroll];
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u)
       if (h + u < h1) {
         const T* row = x + u * p.xs.head;
-        if (kAdjacent) {
-          const Pack<T, 2 * W> v = *reinterpret_cast<const Pack<T, 2 * W>*>(row + lo);
-#pragma unroll
-          for (int j = 0; j < W; ++j) {
-            first[u].v[j] = v.v[2 * j];
-            second[u].v[j] = v.v[2 * j + 1];
-          }
-        } else {
-          first[u] = *reinterpret_cast<const Pack<T, W>*>(row + lo);
-          second[u] = *reinterpret_cast<const Pack<T, W>*>(row + hi);
-        }
+        first[u] = *reinterpret_cast<const Bytes<kRun>*>(row + lo);
+        if (!kAdjacent) second[u] = *reinterpret_cast<const Bytes<kRun>*>(row + hi);
       }
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u)
       if (h + u < h1) {
         T* row = y + u * p.ys.head;
-        Pack<T, W> a = first[u], d = second[u];
-#pragma unroll
-        for (int j = 0; j < W; ++j) {
-          const float xa = to_f32(first[u].v[j]), xb = to_f32(second[u].v[j]);
-          // copied components are not multiplied: an infinity stays one
-          if (!copy[j]) {
-            a.v[j] = from_f32<T>(xa * c[j] - xb * s[j]);
-            d.v[j] = from_f32<T>(xa * s[j] + xb * c[j]);
-          }
-        }
-        if (kAdjacent) {
-          Pack<T, 2 * W> v;
+        if constexpr (kAdjacent) {
+          float f[2 * W];
 #pragma unroll
           for (int j = 0; j < W; ++j) {
-            v.v[2 * j] = a.v[j];
-            v.v[2 * j + 1] = d.v[j];
+            const float xa = element<T>(first[u], 2 * j), xb = element<T>(first[u], 2 * j + 1);
+            f[2 * j] = xa * c[j] - xb * s[j];
+            f[2 * j + 1] = xa * s[j] + xb * c[j];
           }
-          *reinterpret_cast<Pack<T, 2 * W>*>(row + lo) = v;
+          Bytes<kRun> out = run_of<T, kRun>(f);
+          // copied components are taken bit for bit: an infinity, a NaN stays as it is
+          constexpr int kPairWords = (int)sizeof(T) / 2;
+#pragma unroll
+          for (int i = 0; i < kRun / 4; ++i)
+            if (copy[i / kPairWords]) out.w[i] = first[u].w[i];
+          *reinterpret_cast<Bytes<kRun>*>(row + lo) = out;
         } else {
-          *reinterpret_cast<Pack<T, W>*>(row + lo) = a;
-          *reinterpret_cast<Pack<T, W>*>(row + hi) = d;
+          // the run lies in one section: turned or copied as a whole
+          if (!copy[0]) {
+            float f[W], d[W];
+#pragma unroll
+            for (int j = 0; j < W; ++j) {
+              const float xa = element<T>(first[u], j), xb = element<T>(second[u], j);
+              f[j] = xa * c[j] - xb * s[j];
+              d[j] = xa * s[j] + xb * c[j];
+            }
+            first[u] = run_of<T, kRun>(f);
+            second[u] = run_of<T, kRun>(d);
+          }
+          *reinterpret_cast<Bytes<kRun>*>(row + lo) = first[u];
+          *reinterpret_cast<Bytes<kRun>*>(row + hi) = second[u];
         }
       }
     x += kUnroll * p.xs.head;

@@ -27,26 +27,41 @@ __host__ __device__ constexpr bool is_bf16() { return false; }
 template <>
 __host__ __device__ constexpr bool is_bf16<__nv_bfloat16>() { return true; }
 
-// N consecutive elements, loaded and stored as one or more words of up to 16 bytes.
+// N consecutive elements, loaded and stored as words of up to 16 bytes.
 template <typename T, int N>
 struct alignas(sizeof(T) * N < 16 ? sizeof(T) * N : 16) Pack {
   T v[N];
 };
 
-// Eight 16-bit elements held in four words, to fp32.
+// Two fp32 as a word of two 16-bit elements, `lo` in the lower half. (Sixteen-bit data is kept
+// in whole words throughout: arrays of 16-bit elements take a register each, and the packing
+// and unpacking around them doubled the time of the attention for few rows.)
+template <typename T>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  uint32_t r;
+  if (is_bf16<T>())
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  else
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// The two elements of a word.
+template <typename T>
+__device__ __forceinline__ float2 unpack2(uint32_t w) {
+  if (is_bf16<T>())  // bf16 is the upper half of fp32
+    return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+  return __half22float2(*reinterpret_cast<const __half2*>(&w));
+}
+
 template <typename T>
 __device__ __forceinline__ void unpack8(const uint4& u, float (&f)[8]) {
   const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    if (is_bf16<T>()) {  // bf16 is the upper half of fp32
-      f[2 * i] = __uint_as_float(w[i] << 16);
-      f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-    } else {
-      const float2 t = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
-      f[2 * i] = t.x;
-      f[2 * i + 1] = t.y;
-    }
+    const float2 t = unpack2<T>(w[i]);
+    f[2 * i] = t.x;
+    f[2 * i + 1] = t.y;
   }
 }
 
