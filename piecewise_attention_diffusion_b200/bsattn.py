@@ -293,23 +293,25 @@ def bsa_selftest_forward_timeout(Q, K, V, block, row_ptr, col_idx, mode, kbar, v
 
 
 # The calls around the block attention take strided tensors of several types; they run on
-# the tensors' device, whichever device is current.
+# the tensors' device, whichever device is current. Small ones last a few microseconds, so
+# their wrappers pass plain integers and ask torch for little.
 def _strided(t, name, first=None, shape=None):
     """Check a [Bt, H, L, d] tensor (or [Bt, L, N] for a single head) whose last dimension is
     contiguous, of `first`'s type and device; its strides."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if first is not None and (t.dtype != first.dtype or t.device != first.device):
+    if first is None:
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be a CUDA tensor")
+        if t.dtype not in TYPES:
+            raise ValueError(f"{name} must be bfloat16, float16 or float32, got {t.dtype}")
+    elif t.dtype != first.dtype or t.device != first.device:
         raise ValueError(f"{name} must be {first.dtype} on {first.device}, "
                          f"got {t.dtype} on {t.device}")
-    if t.dtype not in TYPES:
-        raise ValueError(f"{name} must be bfloat16, float16 or float32, got {t.dtype}")
     if shape is not None and t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
     st = t.stride()
-    if st[-1] != 1 and t.shape[-1] > 1:
+    if st[-1:] != (1,) and t.shape[-1:] != (1,):
         raise ValueError(f"{name}'s last dimension must be contiguous")
     if len(st) == 4:
         return Strides(st[0], st[1], st[2])
@@ -332,20 +334,32 @@ def _status_ptr(status, device):
     return _plain(status, torch.int32, "status", (1,), device)
 
 
+def _workspace_of(ws, device):
+    """(address, bytes) of a workspace tensor on `device`, or of none."""
+    if ws is None:
+        return None, 0
+    if ws.device != device or not ws.is_contiguous():
+        raise ValueError(f"workspace must be contiguous and on {device}")
+    return ws.data_ptr(), ws.numel() * ws.element_size()
+
+
 def _call(fn, device, stream, *args):
     """lib().fn(*args, stream) with `device` current; on its current stream if none is given."""
+    index = device.index
     if stream is None:
-        raw = torch._C._cuda_getCurrentRawStream(device.index)
+        raw = torch._C._cuda_getCurrentRawStream(index)
     elif stream.device != device:
         raise ValueError(f"the stream is on {stream.device}, the tensors on {device}")
     else:
         raw = stream.cuda_stream
-    f = getattr(lib(), fn)
-    if device.index == torch.cuda.current_device():
-        _check(f(*args, raw), fn)
+    f = getattr(_lib or lib(), fn)
+    if index == torch._C._cuda_getDevice():
+        code = f(*args, raw)
     else:
         with torch.cuda.device(device):
-            _check(f(*args, raw), fn)
+            code = f(*args, raw)
+    if code:
+        raise BsaError(code, fn)
 
 
 def bsa_rotary(X, Y, pos, axis_dims, base=10000.0, pairing=PAIR_ADJACENT, inverse=False,
@@ -403,15 +417,6 @@ def bsa_linear(X, W, Y, bias=None, act=ACT_NONE, gate=None, R=None, workspace=No
 
 def bsa_cross_workspace_bytes(Bt: int, H: int, Hkv: int, Lq: int, Lk: int, d: int) -> int:
     return int(lib().bsa_cross_workspace_bytes(Bt, H, Hkv, Lq, Lk, d))
-
-
-def _workspace_of(ws, device):
-    """(address, bytes) of a workspace tensor on `device`, or of none."""
-    if ws is None:
-        return None, 0
-    if not ws.is_cuda or ws.device != device:
-        raise ValueError(f"workspace must be on {device}")
-    return ws.data_ptr(), ws.numel() * ws.element_size()
 
 
 def bsa_cross_forward(Q, K, V, O, key_len=None, key_mask=None, scale=0.0, lse=None,
@@ -511,11 +516,11 @@ def linear(X, W, bias=None, act=ACT_NONE, gate=None, residual=None, heads=0, sta
     """residual + gate * act(X W^T + bias): X [Bt, L, K], or [Bt, H, L, d] whose heads side by
     side are the K columns; W [N, K]; gate [Bt, N]. Returns [Bt, L, N], with `heads` the
     [Bt, heads, L, N / heads] that the attention takes, or `out` (which may be the residual)."""
+    Bt, L, K, N, _ = _linear_shape(X, W, heads)
     if out is None:
-        Bt, L, K, N, _ = _linear_shape(X, W, heads)
         out = X.new_empty((Bt, heads, L, N // heads) if heads else (Bt, L, N))
     if ws is None:
-        need = bsa_linear_workspace_bytes(X.shape[0], X.shape[-2], W.shape[1], W.shape[0])
+        need = (_lib or lib()).bsa_linear_workspace_bytes(Bt, L, K, N)
         if need:
             ws = torch.empty(need, dtype=torch.uint8, device=X.device)
     bsa_linear(X, W, out, bias, act, gate, residual, ws, status, stream)
@@ -530,8 +535,8 @@ def cross_forward(Q, K, V, key_len=None, key_mask=None, scale=0.0, want_lse=Fals
     O = Q.new_empty(Q.shape) if out is None else out
     lse = Q.new_empty(Q.shape[:3], dtype=torch.float32) if want_lse else None
     if ws is None:
-        need = bsa_cross_workspace_bytes(*Q.shape[:2], K.shape[1], Q.shape[2], K.shape[2],
-                                         Q.shape[3])
+        Bt, H, Lq, d = Q.shape
+        need = (_lib or lib()).bsa_cross_workspace_bytes(Bt, H, K.shape[1], Lq, K.shape[2], d)
         if need:
             ws = torch.empty(need, dtype=torch.uint8, device=Q.device)
     bsa_cross_forward(Q, K, V, O, key_len, key_mask, scale, lse, ws, status, stream)
