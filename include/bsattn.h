@@ -19,7 +19,8 @@
  *   - Tensors are contiguous, row-major [Bt, H, L, d] (page [BSA] §4.3 uses
  *     q, k, v: [B, H, N, D]); Q, K, V and O are bf16; statistics are fp32.
  *     "BH" below is Bt * H, "M" is L / block.
- *   - Every pointer except `desc` is a DEVICE pointer the caller allocated; the
+ *   - Every pointer except `desc`, bsa_strides and `axis_dim`, which are read on the host
+ *     during the call, is a DEVICE pointer the caller allocated; the
  *     library never allocates, frees or synchronises. Device buffers must be 16-byte
  *     aligned.
  *   - Every call is asynchronous on `stream` (a cudaStream_t, NULL = legacy default

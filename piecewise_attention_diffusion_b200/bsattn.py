@@ -371,7 +371,7 @@ def bsa_rotary(X, Y, pos, axis_dims, base=10000.0, pairing=PAIR_ADJACENT, invers
     per = pos.dim() == 3
     pos_ptr = _plain(pos, torch.float32, "pos", (Bt, L, n) if per else (L, n), X.device)
     _call("bsa_rotary", X.device, stream, X.data_ptr(), xs, Y.data_ptr(), ys, TYPES[X.dtype], Bt,
-          H, L, d, pos_ptr, per, n, (_i32 * max(n, 1))(*axis_dims), base, pairing, bool(inverse))
+          H, L, d, pos_ptr, per, n, (_i32 * max(n, 1))(*map(int, axis_dims)), base, pairing, bool(inverse))
 
 
 def bsa_linear_workspace_bytes(Bt: int, L: int, K: int, N: int) -> int:
@@ -499,6 +499,12 @@ def forward(Q, K, V, block, row_ptr, col_idx, csr_per_head, mode, stats=None, sc
     return O, lse
 
 
+def _used_on(stream, t):
+    """Keep what a helper allocated on the current stream until `stream` has used it."""
+    if stream is not None:
+        t.record_stream(stream)
+
+
 def rotary(X, pos, axis_dims, base=10000.0, pairing=PAIR_ADJACENT, inverse=False, out=None,
            stream=None):
     """Rotary positions on [Bt, H, L, d] queries or keys (any strides, such as a projection's
@@ -507,6 +513,7 @@ def rotary(X, pos, axis_dims, base=10000.0, pairing=PAIR_ADJACENT, inverse=False
     itself). inverse turns back, which also takes gradients through the rotation."""
     if out is None:
         out = X.new_empty(X.shape)
+        _used_on(stream, out)
     bsa_rotary(X, out, pos, axis_dims, base, pairing, inverse, stream=stream)
     return out
 
@@ -519,10 +526,12 @@ def linear(X, W, bias=None, act=ACT_NONE, gate=None, residual=None, heads=0, sta
     Bt, L, K, N, _ = _linear_shape(X, W, heads)
     if out is None:
         out = X.new_empty((Bt, heads, L, N // heads) if heads else (Bt, L, N))
+        _used_on(stream, out)
     if ws is None:
         need = (_lib or lib()).bsa_linear_workspace_bytes(Bt, L, K, N)
         if need:
             ws = torch.empty(need, dtype=torch.uint8, device=X.device)
+            _used_on(stream, ws)
     bsa_linear(X, W, out, bias, act, gate, residual, ws, status, stream)
     return out
 
@@ -539,6 +548,11 @@ def cross_forward(Q, K, V, key_len=None, key_mask=None, scale=0.0, want_lse=Fals
         need = (_lib or lib()).bsa_cross_workspace_bytes(Bt, H, K.shape[1], Lq, K.shape[2], d)
         if need:
             ws = torch.empty(need, dtype=torch.uint8, device=Q.device)
+            _used_on(stream, ws)
+    if stream is not None:
+        _used_on(stream, O)
+        if want_lse:
+            _used_on(stream, lse)
     bsa_cross_forward(Q, K, V, O, key_len, key_mask, scale, lse, ws, status, stream)
     return O, lse
 

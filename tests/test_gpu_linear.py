@@ -128,6 +128,15 @@ def test_strided_views_and_what_lies_beside_them(Bt, L):
     _check(b.linear(one, w, gate=gate), one, w, gate=gate)
 
 
+@pytest.mark.parametrize("L,K,N", [(1, 1, 1), (5, 3, 130), (300, 17, 40)])
+def test_sums_shorter_than_their_rows(L, K, N):
+    """K of any size where the rows lie 16 bytes apart: what lies behind K is not read into it."""
+    x = _randn(1, L, 24)
+    w = _randn(N, 32, seed=1)
+    x[..., K:], w[:, K:] = float("nan"), float("inf")
+    _check(b.linear(x[..., :K], w[:, :K]), x[..., :K], w[:, :K])
+
+
 @pytest.mark.parametrize("L,N", [(400, 256), (3, 256), (90, 77)])
 def test_residual_in_place(L, N):
     x, w, r = _randn(2, L, 128), _randn(N, 128, seed=1, scale=0.1), _randn(2, L, N, seed=2)
