@@ -408,6 +408,25 @@ BSA_API bsa_status bsa_cross_forward(const void* Q, const bsa_strides* qs, const
                                      const bsa_strides* os, float* lse, void* workspace,
                                      size_t ws_bytes, int32_t* status, void* stream);
 
+/* bsa_selftest_linear_timeout, bsa_selftest_cross_timeout — the abort paths of bsa_linear's and
+ * bsa_cross_forward's kernels, run without a fault, as bsa_selftest_forward_timeout runs that of
+ * bsa_forward: the same launch sequence on contiguous tensors (X [L, K], W [N, K], Y [L, N], no
+ * bias, gate or residual; Q, O [H, Lq, d], K, V [H, Lk, d]) with every bounded wait limited to
+ * wait_ns. With a limit far below the time of a copy a wait runs out while copies and products
+ * are in flight: the kernel drains, frees TMEM and writes BSA_ERR_TIMEOUT to *status. The output
+ * is then unspecified; the context stays usable.
+ *   wait_ns  1 .. 10^10; status: device int32 the caller zeroes (required). (The kernel of
+ *            bsa_cross_forward for at most four query rows of a key head has no waits.) */
+BSA_API bsa_status bsa_selftest_linear_timeout(const void* X, const void* W, void* Y, int32_t type,
+                                               int32_t L, int32_t K, int32_t N, void* workspace,
+                                               size_t ws_bytes, int64_t wait_ns, int32_t* status,
+                                               void* stream);
+BSA_API bsa_status bsa_selftest_cross_timeout(const void* Q, const void* K, const void* V, void* O,
+                                              int32_t type, int32_t H, int32_t Lq, int32_t Lk,
+                                              int32_t d, const int32_t* key_len, void* workspace,
+                                              size_t ws_bytes, int64_t wait_ns, int32_t* status,
+                                              void* stream);
+
 #ifdef __cplusplus
 }
 #endif

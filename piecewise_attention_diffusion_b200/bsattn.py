@@ -34,7 +34,8 @@ EXPORTS = ("bsa_version", "bsa_status_string", "bsa_mask_blocks", "bsa_workspace
            "bsa_build_mask", "bsa_precompute", "bsa_route", "bsa_forward",
            "bsa_forward_noalloc", "bsa_selftest_wait_timeout", "bsa_selftest_forward_timeout",
            "bsa_rotary", "bsa_linear_workspace_bytes", "bsa_linear",
-           "bsa_cross_workspace_bytes", "bsa_cross_forward")
+           "bsa_cross_workspace_bytes", "bsa_cross_forward", "bsa_selftest_linear_timeout",
+           "bsa_selftest_cross_timeout")
 
 
 class BsaError(RuntimeError):
@@ -83,6 +84,10 @@ _SIGS = {
     "bsa_cross_workspace_bytes": (_sz, [_i32, _i32, _i32, _i32, _i32, _i32]),
     "bsa_cross_forward": (_i32, [_vp, _sp, _vp, _sp, _vp, _sp, _i32, _i32, _i32, _i32, _i32, _i32,
                                  _i32, _vp, _vp, _f32, _vp, _sp, _vp, _vp, _sz, _vp, _vp]),
+    "bsa_selftest_linear_timeout": (_i32, [_vp, _vp, _vp, _i32, _i32, _i32, _i32, _vp, _sz, _i64,
+                                           _vp, _vp]),
+    "bsa_selftest_cross_timeout": (_i32, [_vp, _vp, _vp, _vp, _i32, _i32, _i32, _i32, _i32, _vp,
+                                          _vp, _sz, _i64, _vp, _vp]),
 }
 
 
@@ -436,6 +441,30 @@ def bsa_cross_forward(Q, K, V, O, key_len=None, key_mask=None, scale=0.0, lse=No
           _plain(key_len, torch.int32, "key_len", (Bt,), dev),
           _plain(key_mask, torch.uint8, "key_mask", (Bt, Lk), dev), scale, O.data_ptr(), os_,
           _plain(lse, torch.float32, "lse", (Bt, H, Lq), dev), ws, ws_bytes,
+          _status_ptr(status, dev))
+
+
+def bsa_selftest_linear_timeout(X, W, Y, workspace, wait_ns, status, stream=None):
+    """bsa_linear of X [L, K], W [N, K] with every bounded wait limited to wait_ns: the kernels'
+    abort and drain path, reported as BSA_ERR_TIMEOUT in `status`."""
+    dev = X.device
+    (L, K), N = X.shape, W.shape[0]
+    ws, ws_bytes = _workspace_of(workspace, dev)
+    _call("bsa_selftest_linear_timeout", dev, stream, _plain(X, X.dtype, "X", (L, K), dev),
+          _plain(W, X.dtype, "W", (N, K), dev), _plain(Y, X.dtype, "Y", (L, N), dev),
+          TYPES[X.dtype], L, K, N, ws, ws_bytes, int(wait_ns), _status_ptr(status, dev))
+
+
+def bsa_selftest_cross_timeout(Q, K, V, O, workspace, wait_ns, status, key_len=None, stream=None):
+    """bsa_cross_forward of Q [H, Lq, d], K, V [H, Lk, d] with every bounded wait limited to
+    wait_ns: the kernel's abort and drain path, reported as BSA_ERR_TIMEOUT in `status`."""
+    dev, dt = Q.device, Q.dtype
+    (H, Lq, d), Lk = Q.shape, K.shape[1]
+    ws, ws_bytes = _workspace_of(workspace, dev)
+    _call("bsa_selftest_cross_timeout", dev, stream, _plain(Q, dt, "Q", (H, Lq, d), dev),
+          _plain(K, dt, "K", (H, Lk, d), dev), _plain(V, dt, "V", (H, Lk, d), dev),
+          _plain(O, dt, "O", (H, Lq, d), dev), TYPES[dt], H, Lq, Lk, d,
+          _plain(key_len, torch.int32, "key_len", (1,), dev), ws, ws_bytes, int(wait_ns),
           _status_ptr(status, dev))
 
 

@@ -273,11 +273,12 @@ size_t bsa_linear_workspace_bytes(int32_t Bt, int32_t L, int32_t K, int32_t N) {
   return bsa::linear_workspace(Bt, L, K, N);
 }
 
-bsa_status bsa_linear(const void* X, const bsa_strides* xs, int32_t x_heads, const void* W,
-                      int64_t w_row, const void* bias, int32_t act, const void* gate,
-                      const void* R, const bsa_strides* rs, void* Y, const bsa_strides* ys,
-                      int32_t y_heads, int32_t type, int32_t Bt, int32_t L, int32_t K, int32_t N,
-                      void* workspace, size_t ws_bytes, int32_t* status, void* stream) {
+static bsa_status linear_call(uint64_t wait_ns, const void* X, const bsa_strides* xs,
+                              int32_t x_heads, const void* W, int64_t w_row, const void* bias,
+                              int32_t act, const void* gate, const void* R, const bsa_strides* rs,
+                              void* Y, const bsa_strides* ys, int32_t y_heads, int32_t type,
+                              int32_t Bt, int32_t L, int32_t K, int32_t N, void* workspace,
+                              size_t ws_bytes, int32_t* status, void* stream) {
   if (!X || !W || !Y) return BSA_ERR_INVALID_ARG;
   if (Bt <= 0 || L <= 0 || K <= 0 || N <= 0 || x_heads <= 0 || y_heads <= 0)
     return BSA_ERR_INVALID_ARG;
@@ -295,11 +296,11 @@ bsa_status bsa_linear(const void* X, const bsa_strides* xs, int32_t x_heads, con
   if (!aligned16(X) || !aligned16(W)) return BSA_ERR_INVALID_ARG;
   for (const void* v : {bias, gate, R, static_cast<const void*>(Y)})
     if ((reinterpret_cast<uintptr_t>(v) & 1u) != 0) return BSA_ERR_INVALID_ARG;
-  const bsa::LinearArgs a{X, strides_of(xs, Bt, x_heads, L, K / x_heads), x_heads, W,
+  bsa::LinearArgs a{X, strides_of(xs, Bt, x_heads, L, K / x_heads), x_heads, W,
                           w_row == 0 ? K : w_row, bias, act, gate, R,
                           strides_of(rs, Bt, y_heads, L, N / y_heads), Y,
                           strides_of(ys, Bt, y_heads, L, N / y_heads), y_heads, type, Bt, L, K, N,
-                          workspace, status, 0};
+                          workspace, status, 0, wait_ns};
   if (a.w_row < K || a.w_row >= (int64_t)1 << 39) return BSA_ERR_INVALID_ARG;
   if (N > 1 && a.w_row % 8 != 0) return BSA_ERR_UNSUPPORTED;
   const bsa_status r = check_strides(a.xs, 2);
@@ -317,13 +318,22 @@ bsa_status bsa_linear(const void* X, const bsa_strides* xs, int32_t x_heads, con
   return from_cuda(bsa::launch_linear(a, static_cast<cudaStream_t>(stream)));
 }
 
+bsa_status bsa_linear(const void* X, const bsa_strides* xs, int32_t x_heads, const void* W,
+                      int64_t w_row, const void* bias, int32_t act, const void* gate,
+                      const void* R, const bsa_strides* rs, void* Y, const bsa_strides* ys,
+                      int32_t y_heads, int32_t type, int32_t Bt, int32_t L, int32_t K, int32_t N,
+                      void* workspace, size_t ws_bytes, int32_t* status, void* stream) {
+  return linear_call(0, X, xs, x_heads, W, w_row, bias, act, gate, R, rs, Y, ys, y_heads, type, Bt, L,
+                     K, N, workspace, ws_bytes, status, stream);
+}
+
 size_t bsa_cross_workspace_bytes(int32_t Bt, int32_t H, int32_t Hkv, int32_t Lq, int32_t Lk,
                                  int32_t d) {
   if (check_cross(Bt, H, Hkv, Lq, Lk, d) != BSA_OK) return 0;
   return bsa::cross_workspace(Bt, H, Hkv, Lq, Lk, d);
 }
 
-bsa_status bsa_cross_forward(const void* Q, const bsa_strides* qs, const void* K,
+static bsa_status cross_call(uint64_t wait_ns, const void* Q, const bsa_strides* qs, const void* K,
                              const bsa_strides* ks, const void* V, const bsa_strides* vs,
                              int32_t type, int32_t Bt, int32_t H, int32_t Hkv, int32_t Lq,
                              int32_t Lk, int32_t d, const int32_t* key_len,
@@ -343,7 +353,7 @@ bsa_status bsa_cross_forward(const void* Q, const bsa_strides* qs, const void* K
   bsa::CrossArgs a{Q, strides_of(qs, Bt, H, Lq, d), K, strides_of(ks, Bt, Hkv, Lk, d), V,
                    strides_of(vs, Bt, Hkv, Lk, d), type, Bt, H, Hkv, Lq, Lk, d, key_len, key_mask,
                    bsa::forward_scale(scale, d), O, strides_of(os, Bt, H, Lq, d), lse, workspace,
-                   status};
+                   status, wait_ns};
   for (const bsa_strides& s : {a.qs, a.ks, a.vs, a.os}) {
     r = check_strides(s, 2);
     if (r != BSA_OK) return r;
@@ -356,6 +366,37 @@ bsa_status bsa_cross_forward(const void* Q, const bsa_strides* qs, const void* K
   if (!workspace_ok(bsa::cross_workspace(Bt, H, Hkv, Lq, Lk, d), workspace, ws_bytes))
     return BSA_ERR_WORKSPACE;
   return from_cuda(bsa::launch_cross(a, static_cast<cudaStream_t>(stream)));
+}
+
+bsa_status bsa_cross_forward(const void* Q, const bsa_strides* qs, const void* K,
+                             const bsa_strides* ks, const void* V, const bsa_strides* vs,
+                             int32_t type, int32_t Bt, int32_t H, int32_t Hkv, int32_t Lq,
+                             int32_t Lk, int32_t d, const int32_t* key_len,
+                             const uint8_t* key_mask, float scale, void* O, const bsa_strides* os,
+                             float* lse, void* workspace, size_t ws_bytes, int32_t* status,
+                             void* stream) {
+  return cross_call(0, Q, qs, K, ks, V, vs, type, Bt, H, Hkv, Lq, Lk, d, key_len, key_mask, scale, O,
+                    os, lse, workspace, ws_bytes, status, stream);
+}
+
+bsa_status bsa_selftest_linear_timeout(const void* X, const void* W, void* Y, int32_t type,
+                                       int32_t L, int32_t K, int32_t N, void* workspace,
+                                       size_t ws_bytes, int64_t wait_ns, int32_t* status,
+                                       void* stream) {
+  if (status == nullptr || wait_ns < 1 || wait_ns > 10000000000ll) return BSA_ERR_INVALID_ARG;
+  return linear_call(static_cast<uint64_t>(wait_ns), X, nullptr, 1, W, 0, nullptr, BSA_ACT_NONE,
+                     nullptr, nullptr, nullptr, Y, nullptr, 1, type, 1, L, K, N, workspace, ws_bytes,
+                     status, stream);
+}
+
+bsa_status bsa_selftest_cross_timeout(const void* Q, const void* K, const void* V, void* O,
+                                      int32_t type, int32_t H, int32_t Lq, int32_t Lk, int32_t d,
+                                      const int32_t* key_len, void* workspace, size_t ws_bytes,
+                                      int64_t wait_ns, int32_t* status, void* stream) {
+  if (status == nullptr || wait_ns < 1 || wait_ns > 10000000000ll) return BSA_ERR_INVALID_ARG;
+  return cross_call(static_cast<uint64_t>(wait_ns), Q, nullptr, K, nullptr, V, nullptr, type, 1, H, H,
+                    Lq, Lk, d, key_len, nullptr, 0.f, O, nullptr, nullptr, workspace, ws_bytes,
+                    status, stream);
 }
 
 }  // extern "C"

@@ -761,7 +761,7 @@ cudaError_t run(const CrossArgs& a, cudaStream_t st) {
   p.part_o = part_o;
   p.part_ml = part_ml;
   p.status = a.status;
-  p.wait_ns = kWaitTimeoutNs;
+  p.wait_ns = a.wait_ns > 0 ? a.wait_ns : kWaitTimeoutNs;
   CUtensorMap tmQ, tmK, tmV, tmO;
   bool ok = map_5d<T>(&tmQ, a.Q, D, a.Lq, a.H, a.Bt, a.qs, kBQ, D / 64) &&
             map_5d<T>(&tmO, a.O, D, a.Lq, a.H, a.Bt, a.os, 32, 1);

@@ -114,7 +114,8 @@ struct LinearArgs {
   int y_heads, type, Bt, L, K, N;
   void* ws;
   int32_t* status;
-  int gate_rows;  // set at launch: rows that share one gate vector
+  int gate_rows;         // set at launch: rows that share one gate vector
+  uint64_t wait_ns = 0;  // limit of the kernels' bounded waits; 0: the default
 };
 size_t linear_workspace(int Bt, int L, int K, int N);
 cudaError_t launch_linear(const LinearArgs& a, cudaStream_t st);
@@ -135,6 +136,7 @@ struct CrossArgs {
   float* lse;
   void* ws;
   int32_t* status;
+  uint64_t wait_ns = 0;  // limit of the kernel's bounded waits; 0: the default
 };
 namespace cross {
 // The kernel for few query rows (cross_few.cu): a key head's query heads times Lq at most

@@ -150,15 +150,18 @@ k_linear(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtens
         }
       }
     }
-    // The peer's copies report to the leader, whose last waits below see them land; the
-    // cluster barrier at the end keeps the peer until then.
-    if (!ok && rank == 0) {
+    if (!ok) {
+      // Drain. Both CTAs' copies report to the leader, which waits for those it expected; one
+      // CTA may be ahead of the other by a few, which nobody expected: both leave them a
+      // millisecond, and the cluster barrier at the end keeps both CTAs until then.
       const uint64_t t0 = globaltimer_ns();
       const uint32_t from = issued > (uint32_t)C::NSTAGE ? issued - C::NSTAGE : 0;
-      for (uint32_t r = from; r < issued; ++r)
+      for (uint32_t r = from; r < issued && rank == 0; ++r)
         while (!mbar_try_wait(&bars.full[r % C::NSTAGE], (r / C::NSTAGE) & 1) &&
                globaltimer_ns() - t0 < 100000000ull) {
         }
+      while (globaltimer_ns() - t0 < 1000000ull) {
+      }
       __syncwarp();
     }
   } else if (warp == 1) {

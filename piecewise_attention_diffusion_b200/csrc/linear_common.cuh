@@ -206,7 +206,7 @@ Params<T> params_of(const LinearArgs& a, const Plan& plan) {
   p.part = align32(a.ws);
   p.part_rows = std::min(a.L, plan.rows);
   p.status = a.status;
-  p.wait_ns = kWaitTimeoutNs;
+  p.wait_ns = a.wait_ns > 0 ? a.wait_ns : kWaitTimeoutNs;
   return p;
 }
 

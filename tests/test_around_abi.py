@@ -124,3 +124,14 @@ def test_cross_workspace_sizes():
     assert b.bsa_cross_workspace_bytes(1, 2, 2, 1, 32768, 64) > 0
     assert b.bsa_cross_workspace_bytes(1, 3, 2, 1, 32768, 64) == 0        # refused shapes
     assert b.bsa_cross_workspace_bytes(1, 2, 2, 1, 32768, 96) == 0
+
+
+def test_timeout_selftests_refuse():
+    lin, cro = b.lib().bsa_selftest_linear_timeout, b.lib().bsa_selftest_cross_timeout
+    for wait in (0, -1, 10 ** 10 + 1):
+        assert lin(P, P, P, 0, 8, 64, 64, P, 1 << 40, wait, P, None) == b.ERR_INVALID_ARG
+        assert cro(P, P, P, P, 0, 2, 8, 64, 64, None, P, 1 << 40, wait, P, None) == b.ERR_INVALID_ARG
+    assert lin(P, P, P, 0, 8, 64, 64, P, 1 << 40, 100, None, None) == b.ERR_INVALID_ARG
+    assert cro(P, P, P, P, 0, 2, 8, 64, 64, None, P, 1 << 40, 100, None, None) == b.ERR_INVALID_ARG
+    assert lin(P, P, P, 2, 8, 64, 64, P, 1 << 40, 100, P, None) == b.ERR_UNSUPPORTED
+    assert cro(P, P, P, P, 0, 2, 8, 64, 96, None, P, 1 << 40, 100, P, None) == b.ERR_UNSUPPORTED
