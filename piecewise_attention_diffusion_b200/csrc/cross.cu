@@ -121,7 +121,7 @@ __device__ __forceinline__ void excluded(const Params& p, const Item& it, int t,
 struct Barriers {
   uint64_t k_full[4], k_empty[4], v_full[4], v_empty[4], v_clear[4];
   uint64_t q_full[kStreams];
-  uint64_t s_full[kStreams], p_full[kStreams];
+  uint64_t s_full[kStreams], p_full[kStreams], p_half[kStreams];
   uint64_t o_final[kStreams], o_free[kStreams], q_empty[kStreams];
   uint64_t done;
 };
@@ -167,11 +167,11 @@ __device__ __forceinline__ float2 ex2_poly4(float2 x) {
 // unit, which alone would need as long as the products (128 x 128 exponentials at 16 a cycle).
 constexpr int kPolyOf8 = 2;
 
-// P of one row: 2^(s * scale_log2 - m_ref), to TMEM in pairs of T at p_addr; returns the fp32
-// sum.
+// P of one row: 2^(s * scale_log2 - m_ref), to TMEM in pairs of T at p_addr, arriving at `half`
+// when the first 64 keys are there; returns the fp32 sum.
 template <typename T, int kPoly>
 __device__ __forceinline__ float row_exp(const uint32_t (&r)[kBK], float scale_log2, float m_ref,
-                                         uint32_t p_addr) {
+                                         uint32_t p_addr, uint64_t* half) {
   const float2 sc = make_float2(scale_log2, scale_log2), nm = make_float2(-m_ref, -m_ref);
   float2 acc[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f),
                    make_float2(0.f, 0.f)};
@@ -187,6 +187,11 @@ __device__ __forceinline__ float row_exp(const uint32_t (&r)[kBK], float scale_l
       pk[q] = pack2<T>(v.x, v.y);
     }
     tmem_st32(p_addr + h * 32, pk);
+    if (h == 0) {
+      tmem_wait_st();
+      tc_fence_before();
+      mbar_arrive(half);
+    }
   }
   const float2 a = add2(add2(acc[0], acc[1]), add2(acc[2], acc[3]));
   return a.x + a.y;
@@ -242,6 +247,7 @@ k_cross(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtenso
       mbar_init(&bars.q_full[x], 1);
       mbar_init(&bars.s_full[x], 1);
       mbar_init(&bars.p_full[x], 128);
+      mbar_init(&bars.p_half[x], 128);
       mbar_init(&bars.o_final[x], 1);
       mbar_init(&bars.o_free[x], 128);
       mbar_init(&bars.q_empty[x], 1);
@@ -387,38 +393,57 @@ k_cross(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtenso
         for (int t = 0; t < it.n && ok; ++t) {
           const bool more = t + 1 < it.n;
           const uint32_t vs = nv % C::NV, ks = nk % C::NK;
-          // V(t), cleared of what is masked where there are masks, and K(t + 1)
-          ok = mbar_wait_warp(&bars.v_full[vs], (nv / C::NV) & 1, abort_flag, p.wait_ns) &&
-               (!clearing ||
-                mbar_wait_warp(&bars.v_clear[vs], (nv / C::NV) & 1, abort_flag, p.wait_ns)) &&
-               (!more || mbar_wait_warp(&bars.k_full[ks], (nk / C::NK) & 1, abort_flag, p.wait_ns));
+          const uint32_t v_par = (nv / C::NV) & 1, k_par = (nk / C::NK) & 1;
 #pragma unroll
           for (int x = 0; x < kStreams; ++x) {
             if (x >= ns || !ok) break;
-            ok = mbar_wait_warp(&bars.p_full[x], p_count[x] & 1, abort_flag, p.wait_ns) &&
-                 (t > 0 || items[x] == 1 ||  // the stream's last epilogue has read O
-                  mbar_wait_warp(&bars.o_free[x], (items[x] - 2) & 1, abort_flag, p.wait_ns));
+            // P of the first 64 keys is written; V(t), cleared of what is masked where there are
+            // masks, and K(t + 1); the stream's last epilogue has read O. All are tested at once: a
+            // test takes 107 cycles even of a barrier long complete. (Products from half of P on,
+            // and this, took 16384 x 512 keys from 170 to 163 us.)
+            const bool first = x == 0, o_wait = t == 0 && items[x] > 1;
+            const uint32_t p_par = p_count[x] & 1, o_par = (items[x] - 2) & 1;
+            bool ready = mbar_try_wait(&bars.p_half[x], p_par);
+            if (first) ready &= mbar_try_wait(&bars.v_full[vs], v_par);
+            if (first && clearing) ready &= mbar_try_wait(&bars.v_clear[vs], v_par);
+            if (first && more) ready &= mbar_try_wait(&bars.k_full[ks], k_par);
+            if (o_wait) ready &= mbar_try_wait(&bars.o_free[x], o_par);
+            if (!__all_sync(0xffffffffu, ready))
+              ok = (!first ||
+                    (mbar_wait_warp(&bars.v_full[vs], v_par, abort_flag, p.wait_ns) &&
+                     (!clearing ||
+                      mbar_wait_warp(&bars.v_clear[vs], v_par, abort_flag, p.wait_ns)) &&
+                     (!more || mbar_wait_warp(&bars.k_full[ks], k_par, abort_flag, p.wait_ns)))) &&
+                   (!o_wait || mbar_wait_warp(&bars.o_free[x], o_par, abort_flag, p.wait_ns)) &&
+                   mbar_wait_warp(&bars.p_half[x], p_par, abort_flag, p.wait_ns);
+            if (!ok) break;
+            tc_fence_after();
+            const uint64_t b0 = v_desc + (uint64_t)(vs * (C::SLOT >> 4));
+            if (elect_one()) {
+#pragma unroll
+              for (int k = 0; k < kBK / 32; ++k)  // the first half of P
+                mma_ts(tmem + C::O_COL(x), tmem + C::S_COL(x) + k * 8, b0 + (uint64_t)(k * 128),
+                       idesc_o, t > 0 || k > 0 ? 1u : 0u);
+            }
+            __syncwarp();
+            ok = mbar_wait_warp(&bars.p_full[x], p_count[x] & 1, abort_flag, p.wait_ns);
             if (!ok) break;
             ++p_count[x];
             tc_fence_after();
             if (elect_one()) {
-              const uint64_t b0 = v_desc + (uint64_t)(vs * (C::SLOT >> 4));
 #pragma unroll
-              for (int k = 0; k < kBK / 16; ++k)
+              for (int k = kBK / 32; k < kBK / 16; ++k)
                 mma_ts(tmem + C::O_COL(x), tmem + C::S_COL(x) + k * 8, b0 + (uint64_t)(k * 128),
                        idesc_o, t > 0 || k > 0 ? 1u : 0u);
+              if (!more) mma_commit(&bars.o_final[x]);
+              if (x + 1 == ns) mma_commit(&bars.v_empty[vs]);
               if (more) issue_s(x, ks);
-              else mma_commit(&bars.o_final[x]);
+              if (more && x + 1 == ns) mma_commit(&bars.k_empty[ks]);
               if (t + 2 == it.n) mma_commit(&bars.q_empty[x]);
             }
             __syncwarp();
           }
           if (!ok) break;
-          if (elect_one()) {
-            mma_commit(&bars.v_empty[vs]);
-            if (more) mma_commit(&bars.k_empty[ks]);
-          }
-          __syncwarp();
           ++nv;
           nk += more;
         }
@@ -525,9 +550,9 @@ k_cross(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtenso
         const float m_ref = m_run == -INFINITY ? 0.f : m_run - kLift;
         // NaN and +inf only come out right on the special-function unit
         if (__any_sync(0xffffffffu, !(mx < INFINITY)))
-          l += row_exp<T, 0>(r, p.scale_log2, m_ref, s_base);
+          l += row_exp<T, 0>(r, p.scale_log2, m_ref, s_base, &bars.p_half[x]);
         else
-          l += row_exp<T, kPolyOf8>(r, p.scale_log2, m_ref, s_base);
+          l += row_exp<T, kPolyOf8>(r, p.scale_log2, m_ref, s_base, &bars.p_half[x]);
         tmem_wait_st();
         tc_fence_before();
         mbar_arrive(&bars.p_full[x]);
