@@ -154,6 +154,29 @@ def test_keys_that_are_not_real(size, kind, dtype):
     assert not o[empty].any() and (lse[empty] == float("-inf")).all()
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("scale,sign", [(1e-3, 0), (0.3, 0), (1.0, 1), (1.0, -1), (6.0, -1), (25.0, 0)])
+@pytest.mark.parametrize("kept", [0.03, 0.5, 0.97])
+def test_masked_scores_against_any_reference(dtype, d, scale, sign, kept):
+    """Scores near 0, all positive, all (far) negative and large ones, with few and many keys
+    masked: whatever the masked keys hold must not reach the rows' references nor their sums."""
+    Lq, Lk = 131, 650
+    q, k, v = (_randn(1, 2, n, d, dtype=dtype, seed=s) for n, s in ((Lq, 0), (Lk, 1), (Lk, 2)))
+    if sign:   # |q| and +-|k|: every score has this sign
+        q, k = q.abs(), k.abs() * sign
+    q = (q.float() * scale).to(dtype)
+    g = torch.Generator().manual_seed(int(kept * 100) + d)
+    mask = (torch.rand(1, Lk, generator=g) < kept).to(torch.uint8).to(DEV)
+    mask[0, 130:256] = 0          # a tile with two real keys at most, then one with none
+    mask[0, 256:384] = 0
+    k[:, :, 384:][:, :, mask[0, 384:] == 0] = float("nan")
+    k[:, :, :130][:, :, mask[0, :130] == 0] *= -50.0
+    o, lse = b.cross_forward(q, k, v, key_mask=mask, want_lse=True)
+    z = torch.zeros((), dtype=dtype, device=DEV)
+    _check(o, lse, q, torch.where(torch.isfinite(k), k, z), v, key_mask=mask)
+
+
 @pytest.mark.parametrize("Lq", [140, 2])
 def test_counts_out_of_range_are_reported_and_clamped(Lq):
     q, k, v = _randn(3, 2, Lq, 64), _randn(3, 2, 1100, 64, seed=1), _randn(3, 2, 1100, 64, seed=2)
