@@ -12,6 +12,7 @@ fallback implementation.
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 import os
 
@@ -300,9 +301,9 @@ def bsa_selftest_forward_timeout(Q, K, V, block, row_ptr, col_idx, mode, kbar, v
 # The calls around the block attention take strided tensors of several types; they run on
 # the tensors' device, whichever device is current. Small ones last a few microseconds, so
 # their wrappers pass plain integers and ask torch for little.
-def _strided(t, name, first=None, shape=None):
+def _view(t, name, first=None, shape=None):
     """Check a [Bt, H, L, d] tensor (or [Bt, L, N] for a single head) whose last dimension is
-    contiguous, of `first`'s type and device; its strides."""
+    contiguous, of `first`'s type and device; its strides, None if it is contiguous."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if first is None:
@@ -310,73 +311,86 @@ def _strided(t, name, first=None, shape=None):
             raise ValueError(f"{name} must be a CUDA tensor")
         if t.dtype not in TYPES:
             raise ValueError(f"{name} must be bfloat16, float16 or float32, got {t.dtype}")
-    elif t.dtype != first.dtype or t.device != first.device:
+    elif t.dtype != first.dtype or t.get_device() != first.get_device():
         raise ValueError(f"{name} must be {first.dtype} on {first.device}, "
                          f"got {t.dtype} on {t.device}")
     if shape is not None and t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
     st = t.stride()
-    if st[-1:] != (1,) and t.shape[-1:] != (1,):
+    n = len(st)
+    if n != 4 and n != 3:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected [Bt, H, L, d]")
+    if t.is_contiguous():
+        return None
+    if st[-1] != 1 and t.shape[-1] != 1:
         raise ValueError(f"{name}'s last dimension must be contiguous")
-    if len(st) == 4:
-        return Strides(st[0], st[1], st[2])
-    if len(st) == 3:
-        return Strides(st[0], 0, st[1])
-    raise ValueError(f"{name} has shape {tuple(t.shape)}, expected [Bt, H, L, d]")
+    return Strides(st[0], st[1], st[2]) if n == 4 else Strides(st[0], 0, st[1])
 
 
-def _plain(t, dtype, name, shape, device):
-    """The address of a contiguous tensor of this type and shape on `device`; None for None."""
+def _plain(t, dtype, name, shape, index):
+    """The address of a contiguous tensor of this type and shape on device `index`; None for
+    None."""
     if t is None:
         return None
     _need(t, dtype, name, shape)
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if t.get_device() != index:
+        raise ValueError(f"{name} is on {t.device}, expected device {index}")
     return t.data_ptr()
 
 
-def _status_ptr(status, device):
-    return _plain(status, torch.int32, "status", (1,), device)
-
-
-def _workspace_of(ws, device):
-    """(address, bytes) of a workspace tensor on `device`, or of none."""
+def _workspace_of(ws, index):
+    """(address, bytes) of a workspace tensor on device `index`, or of none."""
     if ws is None:
         return None, 0
-    if ws.device != device or not ws.is_contiguous():
-        raise ValueError(f"workspace must be contiguous and on {device}")
+    if ws.get_device() != index or not ws.is_contiguous():
+        raise ValueError(f"workspace must be contiguous and on device {index}")
     return ws.data_ptr(), ws.numel() * ws.element_size()
 
 
-def _call(fn, device, stream, *args):
-    """lib().fn(*args, stream) with `device` current; on its current stream if none is given."""
-    index = device.index
+def _call(fn, index, stream, *args):
+    """lib().fn(*args, stream) with device `index` current; on its current stream if none is
+    given."""
     if stream is None:
         raw = torch._C._cuda_getCurrentRawStream(index)
-    elif stream.device != device:
-        raise ValueError(f"the stream is on {stream.device}, the tensors on {device}")
+    elif stream.device.index != index:
+        raise ValueError(f"the stream is on {stream.device}, the tensors on device {index}")
     else:
         raw = stream.cuda_stream
     f = getattr(_lib or lib(), fn)
     if index == torch._C._cuda_getDevice():
         code = f(*args, raw)
     else:
-        with torch.cuda.device(device):
+        with torch.cuda.device(index):
             code = f(*args, raw)
     if code:
         raise BsaError(code, fn)
 
 
+@functools.lru_cache(maxsize=64)
+def _int_array(values):
+    return (_i32 * max(len(values), 1))(*map(int, values))
+
+
+def _rotary(X, xs, Y, ys, pos, axis_dims, base, pairing, inverse, stream):
+    Bt, H, L, d = X.shape
+    n, index = len(axis_dims), X.get_device()
+    per = pos.dim() == 3
+    pos_ptr = _plain(pos, torch.float32, "pos", (Bt, L, n) if per else (L, n), index)
+    _call("bsa_rotary", index, stream, X.data_ptr(), xs, Y.data_ptr(), ys, TYPES[X.dtype], Bt, H, L,
+          d, pos_ptr, per, n, _int_array(tuple(axis_dims)), base, pairing, bool(inverse))
+
+
+def _four(t, name):
+    if t.dim() != 4:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected [Bt, H, L, d]")
+
+
 def bsa_rotary(X, Y, pos, axis_dims, base=10000.0, pairing=PAIR_ADJACENT, inverse=False,
                stream=None):
-    xs = _strided(X, "X")
-    Bt, H, L, d = X.shape
-    ys = xs if Y is X else _strided(Y, "Y", X, X.shape)
-    n = len(axis_dims)
-    per = pos.dim() == 3
-    pos_ptr = _plain(pos, torch.float32, "pos", (Bt, L, n) if per else (L, n), X.device)
-    _call("bsa_rotary", X.device, stream, X.data_ptr(), xs, Y.data_ptr(), ys, TYPES[X.dtype], Bt,
-          H, L, d, pos_ptr, per, n, (_i32 * max(n, 1))(*map(int, axis_dims)), base, pairing, bool(inverse))
+    xs = _view(X, "X")
+    _four(X, "X")
+    _rotary(X, xs, Y, xs if Y is X else _view(Y, "Y", X, X.shape), pos, axis_dims, base, pairing,
+            inverse, stream)
 
 
 def bsa_linear_workspace_bytes(Bt: int, L: int, K: int, N: int) -> int:
@@ -387,85 +401,95 @@ def _linear_shape(X, W, y_heads):
     """(Bt, L, K, N, x_heads) of X [Bt, L, K] or [Bt, H, L, d] and W [N, K]."""
     if not isinstance(W, torch.Tensor) or W.dim() != 2:
         raise ValueError("W must be a [N, K] tensor")
-    Bt, L = X.shape[0], X.shape[-2]
-    x_heads = X.shape[1] if X.dim() == 4 else 1
+    shape = X.shape
+    x_heads = shape[1] if len(shape) == 4 else 1
     N, K = W.shape
-    if K != x_heads * X.shape[-1]:
-        raise ValueError(f"W has shape {tuple(W.shape)}, X {tuple(X.shape)}")
+    if K != x_heads * shape[-1]:
+        raise ValueError(f"W has shape {tuple(W.shape)}, X {tuple(shape)}")
     if y_heads and N % y_heads:
         raise ValueError(f"{N} columns do not divide into {y_heads} heads")
-    return Bt, L, K, N, x_heads
+    return shape[0], shape[-2], K, N, x_heads
+
+
+def _linear(X, xs, W, Y, ys, y_heads, dims, bias, act, gate, R, ws, ws_bytes, status, stream):
+    Bt, L, K, N, x_heads = dims
+    index, dtype = X.get_device(), X.dtype
+    if W.dtype != dtype or W.get_device() != index:
+        raise ValueError(f"W must be {dtype} on {X.device}, got {W.dtype} on {W.device}")
+    row, last = W.stride()
+    if last != 1 and K > 1:
+        raise ValueError("W's rows must be contiguous")
+    rs = None if R is None else ys if R is Y else _view(R, "R", X, Y.shape)
+    _call("bsa_linear", index, stream, X.data_ptr(), xs, x_heads, W.data_ptr(), row if N > 1 else 0,
+          _plain(bias, dtype, "bias", (N,), index), act, _plain(gate, dtype, "gate", (Bt, N), index),
+          None if R is None else R.data_ptr(), rs, Y.data_ptr(), ys, y_heads, TYPES[dtype], Bt, L, K,
+          N, ws, ws_bytes, _plain(status, torch.int32, "status", (1,), index))
 
 
 def bsa_linear(X, W, Y, bias=None, act=ACT_NONE, gate=None, R=None, workspace=None, status=None,
                stream=None):
-    xs = _strided(X, "X")
-    ys = _strided(Y, "Y", X)
-    y_heads = Y.shape[1] if Y.dim() == 4 else 1
-    Bt, L, K, N, x_heads = _linear_shape(X, W, y_heads)
-    want = (Bt, y_heads, L, N // y_heads) if Y.dim() == 4 else (Bt, L, N)
+    xs = _view(X, "X")
+    ys = _view(Y, "Y", X)
+    heads = Y.shape[1] if Y.dim() == 4 else 1
+    dims = Bt, L, K, N, _ = _linear_shape(X, W, heads)
+    want = (Bt, heads, L, N // heads) if Y.dim() == 4 else (Bt, L, N)
     if Y.shape != want:
         raise ValueError(f"Y has shape {tuple(Y.shape)}, expected {want}")
-    dev, dtype = X.device, X.dtype
-    if not W.is_cuda or W.dtype != dtype or W.device != dev:
-        raise ValueError(f"W must be {dtype} on {dev}, got {W.dtype} on {W.device}")
-    if W.stride(1) != 1 and K > 1:
-        raise ValueError("W's rows must be contiguous")
-    rs = None if R is None else ys if R is Y else _strided(R, "R", X, Y.shape)
-    ws, ws_bytes = _workspace_of(workspace, dev)
-    _call("bsa_linear", dev, stream, X.data_ptr(), xs, x_heads, W.data_ptr(),
-          W.stride(0) if N > 1 else 0, _plain(bias, dtype, "bias", (N,), dev), act,
-          _plain(gate, dtype, "gate", (Bt, N), dev), None if R is None else R.data_ptr(), rs,
-          Y.data_ptr(), ys, y_heads, TYPES[dtype], Bt, L, K, N, ws, ws_bytes,
-          _status_ptr(status, dev))
+    ws, ws_bytes = _workspace_of(workspace, X.get_device())
+    _linear(X, xs, W, Y, ys, heads, dims, bias, act, gate, R, ws, ws_bytes, status, stream)
 
 
 def bsa_cross_workspace_bytes(Bt: int, H: int, Hkv: int, Lq: int, Lk: int, d: int) -> int:
     return int(lib().bsa_cross_workspace_bytes(Bt, H, Hkv, Lq, Lk, d))
 
 
+def _cross(Q, qs, K, V, O, os_, key_len, key_mask, scale, lse, ws, ws_bytes, status, stream):
+    ks = _view(K, "K", Q)
+    vs = _view(V, "V", Q, K.shape)
+    Bt, H, Lq, d = Q.shape
+    if K.dim() != 4 or K.shape[0] != Bt or K.shape[3] != d:
+        raise ValueError(f"K has shape {tuple(K.shape)}, Q {tuple(Q.shape)}")
+    Hkv, Lk = K.shape[1], K.shape[2]
+    index = Q.get_device()
+    _call("bsa_cross_forward", index, stream, Q.data_ptr(), qs, K.data_ptr(), ks, V.data_ptr(), vs,
+          TYPES[Q.dtype], Bt, H, Hkv, Lq, Lk, d,
+          _plain(key_len, torch.int32, "key_len", (Bt,), index),
+          _plain(key_mask, torch.uint8, "key_mask", (Bt, Lk), index), scale, O.data_ptr(), os_,
+          _plain(lse, torch.float32, "lse", (Bt, H, Lq), index), ws, ws_bytes,
+          _plain(status, torch.int32, "status", (1,), index))
+
+
 def bsa_cross_forward(Q, K, V, O, key_len=None, key_mask=None, scale=0.0, lse=None,
                       workspace=None, status=None, stream=None):
-    qs = _strided(Q, "Q")
-    ks = _strided(K, "K", Q)
-    vs = _strided(V, "V", Q, K.shape)
-    os_ = _strided(O, "O", Q, Q.shape)
-    Bt, H, Lq, d = Q.shape
-    Hkv, Lk = K.shape[1], K.shape[2]
-    if K.shape[0] != Bt or K.shape[3] != d:
-        raise ValueError(f"K has shape {tuple(K.shape)}, Q {tuple(Q.shape)}")
-    dev = Q.device
-    ws, ws_bytes = _workspace_of(workspace, dev)
-    _call("bsa_cross_forward", dev, stream, Q.data_ptr(), qs, K.data_ptr(), ks, V.data_ptr(), vs,
-          TYPES[Q.dtype], Bt, H, Hkv, Lq, Lk, d,
-          _plain(key_len, torch.int32, "key_len", (Bt,), dev),
-          _plain(key_mask, torch.uint8, "key_mask", (Bt, Lk), dev), scale, O.data_ptr(), os_,
-          _plain(lse, torch.float32, "lse", (Bt, H, Lq), dev), ws, ws_bytes,
-          _status_ptr(status, dev))
+    qs = _view(Q, "Q")
+    _four(Q, "Q")
+    os_ = _view(O, "O", Q, Q.shape)
+    ws, ws_bytes = _workspace_of(workspace, Q.get_device())
+    _cross(Q, qs, K, V, O, os_, key_len, key_mask, scale, lse, ws, ws_bytes, status, stream)
 
 
 def bsa_selftest_linear_timeout(X, W, Y, workspace, wait_ns, status, stream=None):
     """bsa_linear of X [L, K], W [N, K] with every bounded wait limited to wait_ns: the kernels'
     abort and drain path, reported as BSA_ERR_TIMEOUT in `status`."""
-    dev = X.device
+    dev = X.get_device()
     (L, K), N = X.shape, W.shape[0]
     ws, ws_bytes = _workspace_of(workspace, dev)
     _call("bsa_selftest_linear_timeout", dev, stream, _plain(X, X.dtype, "X", (L, K), dev),
           _plain(W, X.dtype, "W", (N, K), dev), _plain(Y, X.dtype, "Y", (L, N), dev),
-          TYPES[X.dtype], L, K, N, ws, ws_bytes, int(wait_ns), _status_ptr(status, dev))
+          TYPES[X.dtype], L, K, N, ws, ws_bytes, int(wait_ns), _plain(status, torch.int32, "status", (1,), dev))
 
 
 def bsa_selftest_cross_timeout(Q, K, V, O, workspace, wait_ns, status, key_len=None, stream=None):
     """bsa_cross_forward of Q [H, Lq, d], K, V [H, Lk, d] with every bounded wait limited to
     wait_ns: the kernel's abort and drain path, reported as BSA_ERR_TIMEOUT in `status`."""
-    dev, dt = Q.device, Q.dtype
+    dev, dt = Q.get_device(), Q.dtype
     (H, Lq, d), Lk = Q.shape, K.shape[1]
     ws, ws_bytes = _workspace_of(workspace, dev)
     _call("bsa_selftest_cross_timeout", dev, stream, _plain(Q, dt, "Q", (H, Lq, d), dev),
           _plain(K, dt, "K", (H, Lk, d), dev), _plain(V, dt, "V", (H, Lk, d), dev),
           _plain(O, dt, "O", (H, Lq, d), dev), TYPES[dt], H, Lq, Lk, d,
           _plain(key_len, torch.int32, "key_len", (1,), dev), ws, ws_bytes, int(wait_ns),
-          _status_ptr(status, dev))
+          _plain(status, torch.int32, "status", (1,), dev))
 
 
 # ------------------------------------------------------------ allocating helpers
@@ -540,10 +564,14 @@ def rotary(X, pos, axis_dims, base=10000.0, pairing=PAIR_ADJACENT, inverse=False
     [Bt, L, H, d] transposed): fp32 pos [L, n] or [Bt, L, n], one column per axis, whose
     sections of d are axis_dims. Returns a contiguous [Bt, H, L, d], or `out` (which may be X
     itself). inverse turns back, which also takes gradients through the rotation."""
-    if out is None:
-        out = X.new_empty(X.shape)
-        _used_on(stream, out)
-    bsa_rotary(X, out, pos, axis_dims, base, pairing, inverse, stream=stream)
+    if out is not None:
+        bsa_rotary(X, out, pos, axis_dims, base, pairing, inverse, stream)
+        return out
+    xs = _view(X, "X")
+    _four(X, "X")
+    out = X.new_empty(X.shape)
+    _used_on(stream, out)
+    _rotary(X, xs, out, None, pos, axis_dims, base, pairing, inverse, stream)
     return out
 
 
@@ -552,16 +580,21 @@ def linear(X, W, bias=None, act=ACT_NONE, gate=None, residual=None, heads=0, sta
     """residual + gate * act(X W^T + bias): X [Bt, L, K], or [Bt, H, L, d] whose heads side by
     side are the K columns; W [N, K]; gate [Bt, N]. Returns [Bt, L, N], with `heads` the
     [Bt, heads, L, N / heads] that the attention takes, or `out` (which may be the residual)."""
-    Bt, L, K, N, _ = _linear_shape(X, W, heads)
-    if out is None:
-        out = X.new_empty((Bt, heads, L, N // heads) if heads else (Bt, L, N))
-        _used_on(stream, out)
+    xs = _view(X, "X")
+    dims = Bt, L, K, N, _ = _linear_shape(X, W, heads)
     if ws is None:
         need = (_lib or lib()).bsa_linear_workspace_bytes(Bt, L, K, N)
         if need:
             ws = torch.empty(need, dtype=torch.uint8, device=X.device)
             _used_on(stream, ws)
-    bsa_linear(X, W, out, bias, act, gate, residual, ws, status, stream)
+    if out is not None:
+        bsa_linear(X, W, out, bias, act, gate, residual, ws, status, stream)
+        return out
+    out = X.new_empty((Bt, heads, L, N // heads) if heads else (Bt, L, N))
+    _used_on(stream, out)
+    ptr, ws_bytes = _workspace_of(ws, X.get_device())
+    _linear(X, xs, W, out, None, heads or 1, dims, bias, act, gate, residual, ptr, ws_bytes, status,
+            stream)
     return out
 
 
@@ -570,10 +603,14 @@ def cross_forward(Q, K, V, key_len=None, key_mask=None, scale=0.0, want_lse=Fals
     """Attention of Q [Bt, H, Lq, d] over K, V [Bt, Hkv, Lk, d] (any strides; H a multiple of
     Hkv): the first key_len[b] (int32 [Bt]) keys of each entry, those whose key_mask (uint8
     [Bt, Lk]) is not 0, or all. Returns (O contiguous or `out`, lse fp32 [Bt, H, Lq] or None)."""
-    O = Q.new_empty(Q.shape) if out is None else out
-    lse = Q.new_empty(Q.shape[:3], dtype=torch.float32) if want_lse else None
+    qs = _view(Q, "Q")
+    _four(Q, "Q")
+    if not isinstance(K, torch.Tensor) or K.dim() != 4:
+        raise ValueError("K must be a [Bt, Hkv, Lk, d] tensor")
+    Bt, H, Lq, d = Q.shape
+    O, os_ = (Q.new_empty(Q.shape), None) if out is None else (out, _view(out, "out", Q, Q.shape))
+    lse = Q.new_empty((Bt, H, Lq), dtype=torch.float32) if want_lse else None
     if ws is None:
-        Bt, H, Lq, d = Q.shape
         need = (_lib or lib()).bsa_cross_workspace_bytes(Bt, H, K.shape[1], Lq, K.shape[2], d)
         if need:
             ws = torch.empty(need, dtype=torch.uint8, device=Q.device)
@@ -582,7 +619,8 @@ def cross_forward(Q, K, V, key_len=None, key_mask=None, scale=0.0, want_lse=Fals
         _used_on(stream, O)
         if want_lse:
             _used_on(stream, lse)
-    bsa_cross_forward(Q, K, V, O, key_len, key_mask, scale, lse, ws, status, stream)
+    ptr, ws_bytes = _workspace_of(ws, Q.get_device())
+    _cross(Q, qs, K, V, O, os_, key_len, key_mask, scale, lse, ptr, ws_bytes, status, stream)
     return O, lse
 
 
