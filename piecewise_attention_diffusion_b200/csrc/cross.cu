@@ -21,15 +21,22 @@
 //           (infinities, NaN) meets no product;
 //   warp 10 clears those rows of K where there is a key mask: their scores are then known to be
 //           0, and their share of the sum is taken off as a whole, instead of a select per score
-//           in every tile (288 against 347 us, 2 x 16 heads x 4101 queries x 4352 keys).
+//           in every tile (292 against 347 us, 2 x 16 heads x 4101 queries x 4352 keys).
 // TMEM: S0 [0,128), S1 [128,256), O0 [256, 256 + D), O1 [256 + D, 256 + 2 D); P overlays S.
 // Few rows: the keys are split into runs that separate items take; each leaves its O, m and l
-// in the workspace, and k_join adds them in order.
+// in the workspace, and k_join adds them in order. Query heads that share a key head are taken
+// as one head of more rows where their strides allow it (always for one row; 8 x 40 heads of one
+// query over 8 key heads x 8192 keys x 128: 54 us, a tile for each query head 285).
+// Measured, bf16, K and V read once, out of L2: 40 heads x 16384 queries x 512 keys x 128 in
+// 163 us, 1054 TFLOP/s, the tensor pipe at 53% of its cycles. What bounds it is the chain of one
+// stream's step (scores, maximum, exponentials, P, products: about 2950 cycles for the two
+// streams' 2048 cycles of products), not the exponentials' pipe (41%) nor memory.
 // Every mbarrier wait is bounded; on a timeout the CTA drains, frees TMEM and reports
 // BSA_ERR_TIMEOUT.
 #include <algorithm>
 
 #include "common.cuh"
+#include "cross_share.cuh"
 #include "forward_tiles.cuh"
 #include "internal.h"
 #include "sm100.cuh"
@@ -703,53 +710,87 @@ k_cross(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtenso
   }
 }
 
-// The runs of one row, joined in a fixed order: m = max m_i, o = sum 2^(m_i - m) o_i / l with
-// l = sum 2^(m_i - m) l_i. One warp per row; its lanes take the runs' m and l, 32 at a time.
-template <typename T, int D>
+struct JoinParams {
+  const float* part_o;
+  const float2* part_ml;
+  int64_t rows;
+  int H, Lq;
+  int parts;  // of every row; 0: as sh shares them
+  Shares sh;
+  bsa_strides os;
+  float* lse;
+};
+
+// The parts of one row, joined in a fixed order: m = max m_i, o = sum 2^(m_i - m) o_i / l with
+// l = sum 2^(m_i - m) l_i. W warps per row, each with its own run of parts, whose lanes take the
+// parts' m and l, 32 at a time; eight parts of O are asked for together.
+template <typename T, int D, int W>
 __global__ void __launch_bounds__(128)
-k_join(const float* part_o, const float2* part_ml, int splits, int64_t rows, int H, int Lq, T* o,
-       bsa_strides os, float* lse) {
+k_join(const __grid_constant__ JoinParams p, T* o) {
+  constexpr int V = D / 32;
+  __shared__ float acc_sh[W][D], l_sh[W];
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, w = warp % W;
+  const int64_t row = (int64_t)blockIdx.x * (4 / W) + warp / W;
+  if (row >= p.rows) return;  // whole rows: W = 4 has one row per CTA
+  const int t = (int)(row % p.Lq), h = (int)(row / p.Lq % p.H), b = (int)(row / p.Lq / p.H);
+  const int parts = p.parts > 0 ? p.parts : ceil_div(p.sh.rounds(b), rounds_per_cta(p.sh));
+  const int s1 = ceil_div(parts, W) * (w + 1), end = min(s1, parts);
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int64_t row = (int64_t)blockIdx.x * 4 + threadIdx.x / 32;
-  const int lane = threadIdx.x % 32;
-  if (row >= rows) return;
   float m = -INFINITY;
-  for (int s = lane; s < splits; s += 32) {
-    const float2 ml = part_ml[s * rows + row];
+  for (int s = lane; s < parts; s += 32) {
+    const float2 ml = p.part_ml[s * p.rows + row];
     if (ml.y != 0.f) m = fmaxf(m, ml.x);
   }
   m = warp_max(m);
-  constexpr int V = D / 32;
   float acc[V] = {}, l = 0.f;
-  for (int s0 = 0; s0 < splits; s0 += 32) {
-    float w = 0.f;
-    if (s0 + lane < splits) {
-      const float2 ml = part_ml[(s0 + lane) * rows + row];
+  for (int s0 = s1 - ceil_div(parts, W); s0 < end; s0 += 32) {
+    float weight = 0.f;
+    if (s0 + lane < end) {
+      const float2 ml = p.part_ml[(s0 + lane) * p.rows + row];
       if (ml.y != 0.f) {
-        w = exp2f(ml.x - m);
-        l += w * ml.y;
+        weight = exp2f(ml.x - m);
+        l += weight * ml.y;
       }
     }
-    const int n = min(32, splits - s0);
-#pragma unroll 4
-    for (int s = 0; s < n; ++s) {
-      const float ws = __shfl_sync(0xffffffffu, w, s);
-      if (ws == 0.f) continue;  // no real key in this run: its O was not written
-      const Pack<float, V> part = *reinterpret_cast<const Pack<float, V>*>(
-          part_o + ((s0 + s) * rows + row) * D + lane * V);
+    const int n = min(32, end - s0);
+    for (int s = 0; s < n; s += 8) {
+      Pack<float, V> part[8];
+      float ws[8];
 #pragma unroll
-      for (int e = 0; e < V; ++e) acc[e] += ws * part.v[e];
+      for (int j = 0; j < 8; ++j) {
+        ws[j] = __shfl_sync(0xffffffffu, weight, s + j);
+        if (ws[j] != 0.f)  // else there is no such part, or it has no real key and no O
+          part[j] = *reinterpret_cast<const Pack<float, V>*>(
+              p.part_o + ((s0 + s + j) * p.rows + row) * D + lane * V);
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (ws[j] != 0.f)
+#pragma unroll
+          for (int e = 0; e < V; ++e) acc[e] += ws[j] * part[j].v[e];
     }
   }
   l = warp_sum(l);
+  if constexpr (W > 1) {
+#pragma unroll
+    for (int e = 0; e < V; ++e) acc_sh[w][lane * V + e] = acc[e];
+    if (lane == 0) l_sh[w] = l;
+    __syncthreads();
+    if (w > 0) return;
+#pragma unroll
+    for (int i = 1; i < W; ++i) {
+#pragma unroll
+      for (int e = 0; e < V; ++e) acc[e] += acc_sh[i][lane * V + e];
+      l += l_sh[i];
+    }
+  }
   const float inv = l == 0.f ? 0.f : 1.0f / l;
   Pack<T, V> out;
 #pragma unroll
   for (int e = 0; e < V; ++e) out.v[e] = from_f32<T>(acc[e] * inv);
-  const int t = (int)(row % Lq), h = (int)(row / Lq % H), b = (int)(row / Lq / H);
-  *reinterpret_cast<Pack<T, V>*>(o + b * os.batch + h * os.head + t * os.row + lane * V) = out;
-  if (lane == 0 && lse != nullptr)
-    lse[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
+  *reinterpret_cast<Pack<T, V>*>(o + b * p.os.batch + h * p.os.head + t * p.os.row + lane * V) = out;
+  if (lane == 0 && p.lse != nullptr)
+    p.lse[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
 }
 
 // ------------------------------------------------------------------ host side
@@ -773,25 +814,29 @@ bool map_5d(CUtensorMap* m, const void* ptr, int D, int L, int H, int Bt, const 
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// How a call is run: by k_cross_few or k_cross, and in how many runs of keys.
+// How a call is run: by k_cross_few or k_cross; `parts` per row (1 of k_cross: it writes O), or
+// (k_cross_few, ctas > 0) up to `parts`, as the key counts share `ctas` CTAs.
 struct Plan {
   bool few;
-  int splits;
+  int parts, ctas;
 };
 Plan plan_of(int Bt, int H, int Hkv, int Lq, int Lk) {
   const int sms = fwdtiles::sm_count();
-  if (Lk > 0 && (int64_t)H / Hkv * Lq <= kMostRows && Bt <= 65535 && Hkv <= 65535) {
-    // the runs per head that leave least of the last wave of CTAs empty, 256 keys each at least
+  if (Lk > 0 && (int64_t)H / Hkv * Lq <= kMostRows) {
     const int64_t heads = (int64_t)Bt * Hkv, wave = (int64_t)kFewPerSm * sms;
-    const int most = (int)std::min<int64_t>(std::max<int64_t>(1, 2 * wave / heads),
-                                            std::max(1, Lk / 256));
-    Plan best{true, 1};
+    const int most = std::max(1, Lk / 256);  // 256 keys per CTA at least
+    if (2 * heads <= wave && heads * ceil_div(Lk, 32) < 1 << 25) {
+      const int ctas = (int)std::min(wave, 2 * heads * most);
+      return Plan{true, std::min(ctas / Hkv, ceil_div(Lk, 32)), ctas};
+    }
+    // many heads: the runs per head that leave least of the last wave of CTAs empty
+    Plan best{true, 1, 0};
     double cost = 1e300;
-    for (int s = 1; s <= most; ++s) {
+    for (int s = 1; s <= std::min<int64_t>(most, std::max<int64_t>(1, 4 * wave / heads)); ++s) {
       const double c = (double)((heads * s + wave - 1) / wave) / s + 1e-4 * s;
       if (c < cost) {
         cost = c;
-        best.splits = s;
+        best.parts = s;
       }
     }
     return best;
@@ -800,17 +845,32 @@ Plan plan_of(int Bt, int H, int Hkv, int Lq, int Lk) {
   const int64_t items = (int64_t)Bt * H * ceil_div(Lq, 2 * kBQ);
   const int tiles = ceil_div(Lk, kBK);
   const int64_t want = sms / items;
-  if (want < 2 || tiles < 8) return Plan{false, 1};
+  if (want < 2 || tiles < 8) return Plan{false, 1, 0};
   const int per = ceil_div(tiles, (int)std::min<int64_t>(want, tiles / 4));
-  return Plan{false, ceil_div(tiles, per)};
+  return Plan{false, ceil_div(tiles, per), 0};
+}
+
+Shares shares_of(const CrossArgs& a, const Plan& plan) {
+  return Shares{a.key_len, a.Bt, a.Hkv, a.Lk, few_round(a.d, a.H / a.Hkv * a.Lq), plan.ctas, plan.parts};
 }
 
 template <typename T, int D>
-cudaError_t join(const CrossArgs& a, int splits, const float* part_o, const float2* part_ml,
+cudaError_t join(const CrossArgs& a, const Plan& plan, const float* part_o, const float2* part_ml,
                  cudaStream_t st) {
-  const int64_t rows = (int64_t)a.Bt * a.H * a.Lq;
+  JoinParams p;
+  p.part_o = part_o;
+  p.part_ml = part_ml;
+  p.rows = (int64_t)a.Bt * a.H * a.Lq;
+  p.H = a.H;
+  p.Lq = a.Lq;
+  p.parts = plan.ctas > 0 ? 0 : plan.parts;
+  p.sh = shares_of(a, plan);
+  p.os = a.os;
+  p.lse = a.lse;
+  // four warps per row where the rows are too few to fill the SMs with a warp each
+  const bool wide = p.rows <= 2048;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)((rows + 3) / 4));
+  cfg.gridDim = dim3((unsigned)(wide ? p.rows : (p.rows + 3) / 4));
   cfg.blockDim = dim3(128);
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
@@ -818,8 +878,7 @@ cudaError_t join(const CrossArgs& a, int splits, const float* part_o, const floa
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, k_join<T, D>, part_o, part_ml, splits, rows, a.H, a.Lq,
-                            static_cast<T*>(a.O), a.os, a.lse);
+  return cudaLaunchKernelEx(&cfg, wide ? k_join<T, D, 4> : k_join<T, D, 1>, p, static_cast<T*>(a.O));
 }
 
 template <typename T, int D, bool kKeyMask>
@@ -828,10 +887,10 @@ cudaError_t run(const CrossArgs& a, cudaStream_t st) {
   const Plan plan = plan_of(a.Bt, a.H, a.Hkv, a.Lq, a.Lk);
   const int64_t rows = (int64_t)a.Bt * a.H * a.Lq;
   float* part_o = align32(a.ws);
-  float2* part_ml = reinterpret_cast<float2*>(part_o + plan.splits * rows * D);
+  float2* part_ml = reinterpret_cast<float2*>(part_o + plan.parts * rows * D);
   if (plan.few) {
-    const cudaError_t e = run_few(a, plan.splits, part_o, part_ml, st);
-    return e != cudaSuccess ? e : join<T, D>(a, plan.splits, part_o, part_ml, st);
+    const cudaError_t e = run_few(a, shares_of(a, plan), part_o, part_ml, st);
+    return e != cudaSuccess ? e : join<T, D>(a, plan, part_o, part_ml, st);
   }
   Params p;
   p.Bt = a.Bt;
@@ -840,7 +899,7 @@ cudaError_t run(const CrossArgs& a, cudaStream_t st) {
   p.Lq = a.Lq;
   p.Lk = a.Lk;
   p.q_tiles = ceil_div(a.Lq, 2 * kBQ);
-  p.splits = plan.splits;
+  p.splits = plan.parts;
   p.tiles_per_split = ceil_div(std::max(ceil_div(a.Lk, kBK), 1), p.splits);
   p.n_items = a.Bt * a.H * p.q_tiles * p.splits;
   p.qb = a.qs.batch != 0;
@@ -878,7 +937,7 @@ cudaError_t run(const CrossArgs& a, cudaStream_t st) {
       tmQ, tmK, tmV, tmO, p);
   e = cudaGetLastError();
   if (e != cudaSuccess || p.splits == 1) return e;
-  return join<T, D>(a, p.splits, part_o, part_ml, st);
+  return join<T, D>(a, plan, part_o, part_ml, st);
 }
 
 template <typename T>
@@ -889,14 +948,38 @@ cudaError_t by_shape(const CrossArgs& a, cudaStream_t st) {
 
 }  // namespace cross
 
-size_t cross_workspace(int Bt, int H, int Hkv, int Lq, int Lk, int d) {
-  const cross::Plan plan = cross::plan_of(Bt, H, Hkv, Lq, Lk);
-  if (!plan.few && plan.splits == 1) return 0;
-  const size_t rows = (size_t)Bt * H * Lq;
-  return plan.splits * rows * (d + 2) * sizeof(float) + kAlignSlack;
+// Where the query heads of a key head lie so that (head, row) steps evenly through both Q and O,
+// they are taken as one head of H / Hkv * Lq rows: their tiles then read K and V once for all.
+static bool folds(int H, int Hkv, int Lq, const bsa_strides& s) {
+  return H > Hkv && s.head > 0 && s.head <= ((int64_t)1 << 38) / (H / Hkv) &&
+         (int64_t)H / Hkv * Lq < 1 << 30 && (Lq == 1 || s.head == Lq * s.row);
 }
 
-cudaError_t launch_cross(const CrossArgs& a, cudaStream_t st) {
+static size_t workspace_of(int Bt, int H, int Hkv, int Lq, int Lk, int d) {
+  const cross::Plan plan = cross::plan_of(Bt, H, Hkv, Lq, Lk);
+  if (!plan.few && plan.parts == 1) return 0;
+  const size_t rows = (size_t)Bt * H * Lq;
+  return plan.parts * rows * (d + 2) * sizeof(float) + kAlignSlack;
+}
+
+size_t cross_workspace(int Bt, int H, int Hkv, int Lq, int Lk, int d) {
+  // enough either way: the strides are not known here
+  const int64_t rows = (int64_t)H / Hkv * Lq;
+  const size_t plain = workspace_of(Bt, H, Hkv, Lq, Lk, d);
+  return rows >= 1 << 30 ? plain : std::max(plain, workspace_of(Bt, Hkv, Hkv, (int)rows, Lk, d));
+}
+
+cudaError_t launch_cross(const CrossArgs& args, cudaStream_t st) {
+  CrossArgs a = args;
+  if (folds(a.H, a.Hkv, a.Lq, a.qs) && folds(a.H, a.Hkv, a.Lq, a.os)) {
+    const int share = a.H / a.Hkv;
+    for (bsa_strides* s : {&a.qs, &a.os}) {
+      if (a.Lq == 1) s->row = s->head;
+      s->head *= share;
+    }
+    a.Lq *= share;
+    a.H = a.Hkv;
+  }
   if (a.type == BSA_TYPE_BF16) return cross::by_shape<__nv_bfloat16>(a, st);
   return cross::by_shape<__half>(a, st);
 }

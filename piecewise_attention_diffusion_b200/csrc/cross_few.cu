@@ -10,10 +10,14 @@
 // for the keys it sees, so that nothing is exchanged between keys until the end: then the groups
 // of a warp, and the warps through shared memory, are joined in a fixed order. A key that is not
 // real is not read.
-// The keys of a batch entry are shared by `splits` CTAs; k_join (cross.cu) adds their parts.
+// The keys of a head are shared by CTAs whose parts k_join (cross.cu) adds in order. Each head
+// gets CTAs in proportion to the real keys of its batch entry (cross_share.cuh; every CTA finds
+// the same shares from the key counts), so that short entries leave no SM idle while a long one
+// is read: 8 x 16 heads with 50 to 8192 keys of 8192 x 128 take 56 us, with as many CTAs for each head 99.
 // 2 x 16 heads x 32768 keys x 64: 51 us for 268 MB, 5.2 TB/s (the tensor-core kernel's split
 // tiles: 92 us); with a fifth of the keys masked 53 us (113).
 #include "common.cuh"
+#include "cross_share.cuh"
 #include "internal.h"
 #include "sm100.cuh"
 #include "types.cuh"
@@ -23,14 +27,13 @@ namespace cross {
 
 using sm100::ex2;
 
-constexpr int kFewWarps = 8;
 constexpr int kFewThreads = 32 * kFewWarps;
 
 struct FewParams {
   const void *q, *k, *v;
   bsa_strides qs, ks, vs;
-  int H, Hkv, share, Lq, Lk, splits;
-  const int32_t* key_len;
+  int H, share, Lq;
+  Shares sh;
   const uint8_t* key_mask;
   float scale_log2;
   float* part_o;
@@ -54,21 +57,51 @@ k_cross_few(const __grid_constant__ FewParams p) {
   constexpr int kLanes = D / 8, kKeys = 32 / kLanes;  // lanes per key, keys per warp at a time
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  const int split = blockIdx.x, hk = blockIdx.y, b = blockIdx.z;
   const int c = lane % kLanes * 8, group = lane / kLanes;
   const int rows = p.share * p.Lq;  // <= G
-  int len = p.Lk;
-  if (p.key_len != nullptr) {
-    len = __ldg(p.key_len + b);
-    if ((len < 0 || len > p.Lk) && split == 0 && hk == 0 && threadIdx.x == 0)
-      report(p.status, BSA_ERR_BAD_PADDING);
-    len = min(max(len, 0), p.Lk);
-  }
-  // this CTA's keys, whole rounds of the CTA but at the end
   constexpr int kRound = kFewWarps * kKeys * kAhead;
+  static_assert(kRound == few_round(D, G), "the host counts in the same rounds");
+  __shared__ float o_sh[kFewWarps][G][D];
+  __shared__ float2 ml_sh[kFewWarps][G];
+
+  if (p.sh.key_len != nullptr && blockIdx.x == 0 && warp == 0)
+    for (int i = lane; i < p.sh.Bt; i += 32)
+      if (__ldg(p.sh.key_len + i) != p.sh.len(i)) report(p.status, BSA_ERR_BAD_PADDING);
+  // this CTA's head, and its run of the head's keys, whole rounds of the CTA but at the end
+  int b, hk, split, runs = p.sh.runs;
+  if (p.sh.ctas == 0) {
+    split = blockIdx.x % runs;
+    hk = blockIdx.x / runs % p.sh.Hkv;
+    b = blockIdx.x / runs / p.sh.Hkv;
+  } else {
+    const int per = rounds_per_cta(p.sh);
+    int before = 0;  // CTAs of the entries before b
+    for (b = 0;; b += 32) {
+      runs = b + lane < p.sh.Bt ? ceil_div(p.sh.rounds(b + lane), per) : 0;
+      int to = p.sh.Hkv * runs;
+#pragma unroll
+      for (int w = 1; w < 32; w *= 2) {
+        const int left = __shfl_up_sync(0xffffffffu, to, w);
+        if (lane >= w) to += left;
+      }
+      const uint32_t in = __ballot_sync(0xffffffffu, before + to > (int)blockIdx.x);
+      if (in != 0) {
+        const int at = __ffs(in) - 1;
+        b += at;
+        runs = __shfl_sync(0xffffffffu, runs, at);
+        before += __shfl_sync(0xffffffffu, to, at) - p.sh.Hkv * runs;
+        break;
+      }
+      before += __shfl_sync(0xffffffffu, to, 31);
+      if (b + 32 >= p.sh.Bt) return;  // more CTAs than shares
+    }
+    hk = ((int)blockIdx.x - before) / runs;
+    split = ((int)blockIdx.x - before) % runs;
+  }
+  const int len = p.sh.len(b);
   const int rounds = ceil_div(len, kRound);
-  const int k0 = (int)((int64_t)rounds * split / p.splits) * kRound;
-  const int k1 = min(len, (int)((int64_t)rounds * (split + 1) / p.splits) * kRound);
+  const int k0 = (rounds / runs * split + min(rounds % runs, split)) * kRound;
+  const int k1 = min(len, k0 + (rounds / runs + (split < rounds % runs ? 1 : 0)) * kRound);
 
   float q[G][8], o[G][8], m[G], l[G];
 #pragma unroll
@@ -88,7 +121,7 @@ k_cross_few(const __grid_constant__ FewParams p) {
   }
   const T* kp = static_cast<const T*>(p.k) + b * p.ks.batch + hk * p.ks.head + c;
   const T* vp = static_cast<const T*>(p.v) + b * p.vs.batch + hk * p.vs.head + c;
-  const uint8_t* mask = p.key_mask + (int64_t)b * p.Lk;
+  const uint8_t* mask = p.key_mask + (int64_t)b * p.sh.Lk;
 
   uint4 ku[kAhead], vu[kAhead], kn[kAhead], vn[kAhead];
   bool real[kAhead], next[kAhead];
@@ -171,8 +204,6 @@ k_cross_few(const __grid_constant__ FewParams p) {
         o[r][e] = wa * o[r][e] + wb * __shfl_xor_sync(0xffffffffu, o[r][e], w);
     }
   // the warps
-  __shared__ float o_sh[kFewWarps][G][D];
-  __shared__ float2 ml_sh[kFewWarps][G];
   if (lane < kLanes)
 #pragma unroll
     for (int r = 0; r < G; ++r) {
@@ -201,20 +232,21 @@ k_cross_few(const __grid_constant__ FewParams p) {
 }
 
 template <typename T, int D, int G>
-cudaError_t launch_few(const CrossArgs& a, const FewParams& p, cudaStream_t st) {
-  k_cross_few<T, D, G, G <= 2 ? 4 : 2><<<dim3(p.splits, a.Hkv, a.Bt), kFewThreads, 0, st>>>(p);
+cudaError_t launch_few(int ctas, const FewParams& p, cudaStream_t st) {
+  k_cross_few<T, D, G, G <= 2 ? 4 : 2><<<ctas, kFewThreads, 0, st>>>(p);
   return cudaGetLastError();
 }
 
 template <typename T, int D>
-cudaError_t by_rows(const CrossArgs& a, const FewParams& p, cudaStream_t st) {
+cudaError_t by_rows(int ctas, const FewParams& p, cudaStream_t st) {
   const int rows = p.share * p.Lq;
-  if (rows <= 1) return launch_few<T, D, 1>(a, p, st);
-  if (rows <= 2) return launch_few<T, D, 2>(a, p, st);
-  return launch_few<T, D, 4>(a, p, st);
+  if (rows <= 1) return launch_few<T, D, 1>(ctas, p, st);
+  if (rows <= 2) return launch_few<T, D, 2>(ctas, p, st);
+  return launch_few<T, D, 4>(ctas, p, st);
 }
 
-cudaError_t run_few(const CrossArgs& a, int splits, float* part_o, float2* part_ml, cudaStream_t st) {
+cudaError_t run_few(const CrossArgs& a, const Shares& shares, float* part_o, float2* part_ml,
+                    cudaStream_t st) {
   FewParams p;
   p.q = a.Q;
   p.k = a.K;
@@ -223,21 +255,19 @@ cudaError_t run_few(const CrossArgs& a, int splits, float* part_o, float2* part_
   p.ks = a.ks;
   p.vs = a.vs;
   p.H = a.H;
-  p.Hkv = a.Hkv;
   p.share = a.H / a.Hkv;
   p.Lq = a.Lq;
-  p.Lk = a.Lk;
-  p.splits = splits;
-  p.key_len = a.key_len;
+  p.sh = shares;
   p.key_mask = a.key_mask;
   p.scale_log2 = a.scale * 1.4426950408889634f;
   p.part_o = part_o;
   p.part_ml = part_ml;
   p.status = a.status;
   p.rows_all = (int64_t)a.Bt * a.H * a.Lq;
+  const int ctas = shares.ctas > 0 ? shares.ctas : a.Bt * a.Hkv * shares.runs;
   if (a.type == BSA_TYPE_BF16)
-    return a.d == 64 ? by_rows<__nv_bfloat16, 64>(a, p, st) : by_rows<__nv_bfloat16, 128>(a, p, st);
-  return a.d == 64 ? by_rows<__half, 64>(a, p, st) : by_rows<__half, 128>(a, p, st);
+    return a.d == 64 ? by_rows<__nv_bfloat16, 64>(ctas, p, st) : by_rows<__nv_bfloat16, 128>(ctas, p, st);
+  return a.d == 64 ? by_rows<__half, 64>(ctas, p, st) : by_rows<__half, 128>(ctas, p, st);
 }
 
 }  // namespace cross

@@ -140,9 +140,13 @@ struct CrossArgs {
 };
 namespace cross {
 // The kernel for few query rows (cross_few.cu): a key head's query heads times Lq at most
-// kMostRows; kFewPerSm CTAs share an SM. Leaves `splits` parts per row for k_join.
-constexpr int kMostRows = 4, kFewPerSm = 2;
-cudaError_t run_few(const CrossArgs& a, int splits, float* part_o, float2* part_ml,
+// kMostRows; kFewPerSm CTAs share an SM. The CTAs are shared as `shares` says (cross_share.cuh);
+// each leaves a part for k_join.
+constexpr int kMostRows = 4, kFewPerSm = 2, kFewWarps = 8;
+// Keys per round of a CTA: what its run of keys is counted in.
+constexpr int few_round(int d, int rows) { return kFewWarps * (256 / d) * (rows <= 2 ? 4 : 2); }
+struct Shares;
+cudaError_t run_few(const CrossArgs& a, const Shares& shares, float* part_o, float2* part_ml,
                     cudaStream_t st);
 }  // namespace cross
 size_t cross_workspace(int Bt, int H, int Hkv, int Lq, int Lk, int d);

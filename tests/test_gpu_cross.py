@@ -285,3 +285,51 @@ def test_more_than_2_31_elements_of_keys():
     q = _randn(1, 1, 2, 128, seed=3)
     o, lse = b.cross_forward(q, k, v, key_mask=mask, want_lse=True)
     _check(o, lse, q, k[:, :, -200:], v[:, :, -200:])
+
+
+# key counts that share the CTAs of few query rows: alike, apart, all but one empty, none; more
+# heads than a wave of CTAs; more entries than a warp's lanes; few keys in all
+@pytest.mark.parametrize("size,lens", [
+    ((2, 16, 16, 1, 9000, 64), (9000, 9000)), ((3, 4, 4, 1, 9000, 128), (9000, 1, 0)),
+    ((8, 2, 2, 1, 5000, 64), (0, 0, 0, 4999, 0, 0, 0, 0)), ((3, 2, 1, 2, 4000, 64), (0, 0, 0)),
+    ((40, 1, 1, 3, 1500, 64), tuple(1500 * (i % 3 == 0) + i for i in range(39)) + (7,)),
+    ((100, 1, 1, 1, 700, 128), tuple(7 * i for i in range(100))),
+    ((10, 40, 40, 1, 600, 64), (600, 599, 0, 1, 257, 300, 0, 128, 64, 600)),
+    ((2, 4, 1, 1, 31, 64), (31, 2)), ((149, 1, 1, 1, 300, 64), (300,) * 149)])
+def test_key_counts_share_the_work(size, lens):
+    Bt, H, Hkv, Lq, Lk, d = size
+    q = _randn(Bt, H, Lq, d)
+    k, v = (_randn(Bt, Hkv, Lk, d, seed=s) for s in (1, 2))
+    n = torch.tensor([min(x, Lk) for x in lens], dtype=torch.int32, device=DEV)
+    _spoil(k, v, n, None)
+    st = _st()
+    o, lse = b.cross_forward(q, k, v, key_len=n, want_lse=True, status=st)
+    assert st.item() == 0
+    _check(o, lse, q, k, v, key_len=n)
+    again, _ = b.cross_forward(q, k, v, key_len=n)
+    assert torch.equal(o, again)
+
+
+# query heads that share a key head: one after the other in memory (taken as one head), in rows
+# side by side, with gaps between heads or rows, all heads one copy
+@pytest.mark.parametrize("Lq", [1, 2, 5, 40, 300])
+@pytest.mark.parametrize("layout", ["heads", "rows", "head gaps", "row gaps", "one copy"])
+def test_query_heads_of_one_key_head(Lq, layout):
+    Bt, H, Hkv, Lk, d = 2, 12, 2, 1300, 64
+    q = _randn(Bt, H, Lq, d)
+    if layout == "rows":
+        q = q.transpose(1, 2).contiguous().transpose(1, 2)
+    elif layout == "head gaps":
+        q = _randn(Bt, H, Lq + 3, d)[:, :, :Lq]
+    elif layout == "row gaps":
+        q = _randn(Bt, H, Lq, 2 * d)[..., :d]
+    elif layout == "one copy":
+        q = q[:, :1].expand(Bt, H, Lq, d)
+    k, v = (_randn(Bt, Hkv, Lk, d, seed=s) for s in (1, 2))
+    n = torch.tensor([Lk, 700], dtype=torch.int32, device=DEV)
+    for out in ("heads", "rows"):
+        room = torch.full((Bt, H, Lq, d) if out == "heads" else (Bt, Lq, H, d), 7.0, dtype=q.dtype,
+                          device=DEV)
+        o = room if out == "heads" else room.transpose(1, 2)
+        o, lse = b.cross_forward(q, k, v, key_len=n, want_lse=True, out=o)
+        _check(o, lse, q, k, v, key_len=n)
