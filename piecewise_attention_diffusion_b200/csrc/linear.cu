@@ -14,11 +14,17 @@
 //   warp 0     TMA producer (each CTA its half; both report to the leader's barrier);
 //   warp 1     MMA issuer (leader), TMEM allocation;
 //   warps 2..  epilogue: up to four warps per TMEM lane quadrant, each with its own columns.
-//              Per chunk of 32 columns: accumulators to registers, bias, activation,
-//              gate and residual in fp32, one rounding, then through a swizzled staging
-//              buffer to a TMA store (or coalesced 2-byte stores where Y's strides rule TMA
-//              out). Two TMEM accumulators, so the epilogue of one tile runs under the
-//              products of the next.
+//              The residual comes by TMA into the warp's staging buffer while the products
+//              run; then per chunk of 32 columns: accumulators to registers, bias, activation,
+//              gate and residual in fp32, one rounding, back into the buffer, and a TMA store.
+//              (Where strides rule TMA out: coalesced 2-byte accesses, 16 rows at a time.) Two
+//              TMEM accumulators, so the epilogue of one tile runs under the products of the next.
+// Measured out of L2, bf16: 16384 x 5120 x 5120 with bias, gate and residual 588-690 us (by the
+// power limit; 1.25-1.46 PFLOP/s), the tensor pipe at 93%; 9216 x 1024 x 4096 with GELU 66 us,
+// bound by the epilogue, whose warps wait on one latency after the other (erf form: on its
+// arithmetic); 2928 x 168 x 19968 with a residual 83 us where 16-byte loads of it by the lanes
+// that own its rows took 126. Chunks are 32 columns because boxes of 64 (128-byte rows), stored
+// once per tile, delay the operands' loads: 2.3% more time at K = 5120.
 // Every mbarrier wait is bounded; on a timeout the pair drains, frees TMEM and reports
 // BSA_ERR_TIMEOUT.
 #include <algorithm>
@@ -30,7 +36,7 @@ namespace bsa {
 namespace linear {
 
 constexpr int kBM = 128;      // rows per CTA (256 per pair)
-constexpr int kCW = 32;        // columns per epilogue chunk: rows of 64 bytes in the staging buffer
+constexpr int kCW = 32;       // columns per epilogue chunk
 constexpr int kRowGroup = 8;  // row tiles that a sweep over the columns shares (L2 reuse)
 
 template <int BN>
@@ -43,18 +49,28 @@ struct Cfg {
   static constexpr int COLS = BN / PARTS;
   static constexpr int EPI = 4 * PARTS;
   static constexpr int THREADS = 64 + 32 * EPI;
-  static constexpr int OUT = 32 * kCW * 2;  // staging bytes per epilogue warp: one chunk
+  static constexpr int OUT = 32 * COLS * 2;  // staging bytes per epilogue warp: its columns
   static constexpr int NSTAGE = BN == 256 ? 5 : BN == 128 ? 6 : 9;
-  static constexpr int SMEM = NSTAGE * STAGE + EPI * OUT + 1024;
   static constexpr uint32_t TMEM = 2 * BN;              // two accumulators
 };
 
-constexpr int kMaxStages = 9;
+constexpr int kMaxStages = 9, kMaxEpilogue = 16;
 struct Barriers {
   uint64_t full[kMaxStages], empty[kMaxStages];
   uint64_t acc_full[2], acc_empty[2];
+  uint64_t res_full[kMaxEpilogue];
   uint64_t done;
 };
+// What lies behind the stages and the staging buffers in shared memory.
+template <typename T>
+struct Small {
+  T bias[kMaxEpilogue][kCW], gate[kMaxEpilogue][kCW];  // of a chunk
+  Barriers bars;
+  uint32_t tmem_base;
+  int abort;
+};
+template <typename T, int BN>
+constexpr int kSmem = Cfg<BN>::NSTAGE * Cfg<BN>::STAGE + Cfg<BN>::EPI * Cfg<BN>::OUT + (int)sizeof(Small<T>);
 
 // Row and column tile of work item t: groups of kRowGroup row tiles, within a group column
 // by column, so that the pairs at work at one time share both X's and W's tiles.
@@ -70,16 +86,18 @@ __device__ __forceinline__ void tile_of(const P& p, int t, int& m, int& n) {
 template <typename T, int BN, int kAct>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<BN>::THREADS, 1)
 k_linear(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW,
-         const __grid_constant__ CUtensorMap tmY, const __grid_constant__ Params<T> p) {
+         const __grid_constant__ CUtensorMap tmY, const __grid_constant__ CUtensorMap tmR,
+         const __grid_constant__ Params<T> p) {
   using C = Cfg<BN>;
-  extern __shared__ unsigned char smem_raw[];
-  // the same offset in both CTAs: the window's base is the same for the whole grid
-  unsigned char* smem = reinterpret_cast<unsigned char*>(
-      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  __shared__ Barriers bars;
-  __shared__ uint32_t tmem_base_sh;
-  __shared__ int abort_sh;
-  __shared__ __align__(16) float bias_sh[C::EPI][kCW], gate_sh[C::EPI][kCW];  // of a chunk
+  // all of it, so that the base is the window's, with no room to spare for aligning it
+  extern __shared__ __align__(1024) unsigned char smem[];
+  if (smem_u32(smem) % 1024 != 0) {  // alike in both CTAs
+    if (threadIdx.x == 0) report(p.status, BSA_ERR_CUDA);
+    return;
+  }
+  Small<T>& small = *reinterpret_cast<Small<T>*>(smem + C::NSTAGE * C::STAGE + C::EPI * C::OUT);
+  Barriers& bars = small.bars;
+  int& abort_sh = small.abort;
 
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const uint32_t rank = cluster_rank();
@@ -93,23 +111,25 @@ k_linear(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtens
       mbar_init(&bars.acc_full[i], 1);
       mbar_init(&bars.acc_empty[i], 2 * C::EPI);
     }
+    for (int i = 0; i < C::EPI; ++i) mbar_init(&bars.res_full[i], 1);
     mbar_init(&bars.done, 1);
     fence_barrier_init();
   }
   if (warp == 1) {
-    tmem_alloc_pair(&tmem_base_sh, C::TMEM);
+    tmem_alloc_pair(&small.tmem_base, C::TMEM);
     tmem_relinquish_pair();
   }
   if (warp == 0 && lane == 0) {
     prefetch_tensormap(&tmX);
     prefetch_tensormap(&tmW);
     if (p.tma_out) prefetch_tensormap(&tmY);
+    if (p.tma_res) prefetch_tensormap(&tmR);
   }
   tc_fence_before();
   __syncthreads();
   cluster_sync();
   tc_fence_after();
-  const uint32_t tmem = tmem_base_sh;
+  const uint32_t tmem = small.tmem_base;
   volatile int* abort_flag = &abort_sh;
   const int group = blockIdx.x / 2, groups = gridDim.x / 2;
   // k_finish may take its place now; it waits for this grid before it reads a sum
@@ -219,8 +239,17 @@ k_linear(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtens
     unsigned char* out = smem + C::NSTAGE * C::STAGE + e * C::OUT;
     const uint32_t empty_addr[2] = {cluster_addr(&bars.acc_empty[0], 0),
                                     cluster_addr(&bars.acc_empty[1], 0)};
+    // 16-byte piece g of row r of the staging buffer, which holds a chunk after the other, each of
+    // 64-byte rows in that width's swizzle
+    auto piece = [&](int r, int g) {
+      return out + g / 4 * (32 * kCW * 2) + r * kCW * 2 + (g % 4 ^ ((r >> 1) & 3)) * 16;
+    };
+    auto staged = [&](int r, int col) {
+      return reinterpret_cast<uint16_t*>(piece(r, col / 8) + col % 8 * 2);
+    };
     bool ok = true;
     int it = 0;
+    uint32_t residuals = 0;  // loaded by TMA
     WorkIter iter(p, group, groups);
     for (Work w; iter.next(p, w); ++it) {
       int m, n;
@@ -235,55 +264,61 @@ k_linear(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtens
       const int gate_of = p.gate != nullptr ? (b * p.L + min(row, p.L - 1)) / p.gate_rows : 0;
       const bool one_gate = __all_sync(0xffffffffu, gate_of == __shfl_sync(0xffffffffu, gate_of, 0));
       const T* gate = p.gate + (int64_t)gate_of * p.N;
-      const T* res_row = p.res + b * p.rv.batch + row * p.rv.row;
-      // what a chunk needs besides the accumulators: one column's bias and (shared) gate per
-      // lane, and 32 columns of the row's residual; asked for a chunk ahead
-      struct Ahead {
-        T bias, gate;
-        uint4 res[kCW / 8];
-      } ahead;
+      const bool here = row0 < p.L && tile_col < p.N;  // this warp has outputs in this tile
+      const bool whole = !partial(p, w);
+      // a chunk's bias and (shared) gate, a column per lane, asked for a chunk ahead
+      T bias_ahead, gate_ahead;
       auto fetch = [&](int col0) {
         const bool in = col0 + lane < p.N;
-        ahead.bias = in && p.bias != nullptr ? p.bias[col0 + lane] : from_f32<T>(0.f);
-        ahead.gate = in && p.gate != nullptr && one_gate ? gate[col0 + lane] : from_f32<T>(1.f);
+        bias_ahead = in && p.bias != nullptr ? p.bias[col0 + lane] : from_f32<T>(0.f);
+        gate_ahead = in && p.gate != nullptr && one_gate ? gate[col0 + lane] : from_f32<T>(1.f);
       };
-      auto fetch_res = [&](int col) -> uint4 {
-        const int head = col / p.rv.cols;
-        return *reinterpret_cast<const uint4*>(res_row + head * p.rv.head + (col - head * p.rv.cols));
-      };
-      const bool vec_res = p.vec_res && live;  // then 8 columns are all there or all not
-      const bool rows_here = row0 < p.L;
-      const bool whole = !partial(p, w);
-      // a residual that 16-byte loads cannot take comes through the staging buffer, a row at a
-      // time across the lanes (places past the end repeat the last)
-      auto stage_res = [&](int col0) {
-        const int head = col0 / p.rv.cols;
-        const T* at = p.res + b * p.rv.batch + head * p.rv.head +
-                      (min(col0 + lane, p.N - 1) - head * p.rv.cols);
-#pragma unroll 16
-        for (int rr = 0; rr < 32; ++rr)
-          *reinterpret_cast<T*>(out + rr * kCW * 2 + ((lane / 8) ^ ((rr >> 1) & 3)) * 16 +
-                                lane % 8 * 2) = at[min(row0 + rr, p.L - 1) * p.rv.row];
-      };
-      if (whole && rows_here && tile_col < p.N) {
+      if (whole && here) {
         fetch(tile_col);
-        if (p.res != nullptr && !p.vec_res) {
-          if (lane == 0) bulk_wait_read_all();
-          __syncwarp();
-          stage_res(tile_col);
-        }
+        // R lands where Y is staged, and is replaced by it piece by piece
+        if (lane == 0) bulk_wait_read_all();  // the last store has read the buffer
+        __syncwarp();
+        if (p.tma_res) {
+          if (lane == 0) {
+            const int head = tile_col / p.rv.cols;
+            mbar_arrive_expect_tx(&bars.res_full[e], C::OUT);
+            for (int c = 0; c < C::COLS; c += kCW)
+              tma_load_4d(out + c * 64, &tmR, &bars.res_full[e], tile_col + c - head * p.rv.cols, row0,
+                          head * p.rh, b * p.rb);
+          }
+          ++residuals;
+        } else if (p.res != nullptr) {
+          // a row at a time across the lanes (places past the end repeat the last)
+#pragma unroll 1
+          for (int c = 0; c < C::COLS && tile_col + c < p.N; c += kCW) {
+            const int head = (tile_col + c) / p.rv.cols;
+            const T* at = p.res + b * p.rv.batch + head * p.rv.head + row0 * p.rv.row +
+                          (min(tile_col + c + lane, p.N - 1) - head * p.rv.cols);
+#pragma unroll 1
+            for (int r0 = 0; r0 < 32; r0 += 16) {
+              uint16_t words[16];  // all asked for before the first is used
 #pragma unroll
-        for (int g = 0; g < kCW / 8; ++g)
-          if (vec_res && tile_col + g * 8 < p.N) ahead.res[g] = fetch_res(tile_col + g * 8);
+              for (int i = 0; i < 16; ++i) {
+                words[i] = __ldg(reinterpret_cast<const uint16_t*>(at));
+                if (row0 + r0 + i + 1 < p.L) at += p.rv.row;
+              }
+#pragma unroll
+              for (int i = 0; i < 16; ++i) *staged(r0 + i, c + lane) = words[i];
+            }
+          }
+          __syncwarp();
+        }
       }
       ok = mbar_wait(&bars.acc_full[acc], (it / 2) & 1, abort_flag, p.wait_ns);
+      if (whole && here && p.tma_res && ok)
+        ok = mbar_wait(&bars.res_full[e], (residuals - 1) & 1, abort_flag, p.wait_ns);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
       tc_fence_after();
 #pragma unroll 1
       for (int c = 0; c < C::COLS; c += kCW) {
         const int col0 = tile_col + c;
-        if (col0 >= p.N || !rows_here) break;
+        if (col0 >= p.N || !here) break;
         uint32_t r[kCW];
         tmem_ld32(tmem + ((uint32_t)(quad * 32) << 16) + acc * BN + part * C::COLS + c, r);
         if (!whole) {  // a partial sum: 128 bytes of the slot's row
@@ -299,33 +334,29 @@ k_linear(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtens
                            : "memory");
           continue;
         }
-        bias_sh[e][lane] = to_f32(ahead.bias);
-        gate_sh[e][lane] = to_f32(ahead.gate);
-        const bool more = c + kCW < C::COLS && col0 + kCW < p.N;
-        if (more) fetch(col0 + kCW);
-        if (lane == 0) bulk_wait_read_all();  // the staging buffer's last store has read it
-        __syncwarp();
-        if (c > 0 && p.res != nullptr && !p.vec_res) stage_res(col0);
+        small.bias[e][lane] = bias_ahead;
+        small.gate[e][lane] = gate_ahead;
+        if (c + kCW < C::COLS && col0 + kCW < p.N) fetch(col0 + kCW);
         __syncwarp();
         tmem_wait_ld();
 #pragma unroll
         for (int g = 0; g < kCW / 8; ++g) {
           const int col = col0 + g * 8;
-          // the 64-byte swizzle of the store's box: 16-byte piece g of row r sits at
-          // g ^ (r / 2 % 4)
-          uint4* slot =
-              reinterpret_cast<uint4*>(out + lane * kCW * 2 + (g ^ ((lane >> 1) & 3)) * 16);
+          uint4* slot = reinterpret_cast<uint4*>(piece(lane, c / 8 + g));
+          const uint4 bias8 = *reinterpret_cast<const uint4*>(&small.bias[e][g * 8]);
+          const uint32_t biases[4] = {bias8.x, bias8.y, bias8.z, bias8.w};
           float2 v[4];
 #pragma unroll
           for (int i = 0; i < 4; ++i)
             v[i] = activate<kAct>(add2(make_float2(__uint_as_float(r[g * 8 + 2 * i]),
                                                    __uint_as_float(r[g * 8 + 2 * i + 1])),
-                                       *reinterpret_cast<float2*>(&bias_sh[e][g * 8 + 2 * i])));
+                                       unpack2<T>(biases[i])));
           if (p.gate != nullptr) {
             if (one_gate) {
+              const uint4 gate8 = *reinterpret_cast<const uint4*>(&small.gate[e][g * 8]);
+              const uint32_t gates[4] = {gate8.x, gate8.y, gate8.z, gate8.w};
 #pragma unroll
-              for (int i = 0; i < 4; ++i)
-                v[i] = mul2(v[i], *reinterpret_cast<float2*>(&gate_sh[e][g * 8 + 2 * i]));
+              for (int i = 0; i < 4; ++i) v[i] = mul2(v[i], unpack2<T>(gates[i]));
             } else {
 #pragma unroll
               for (int i = 0; i < 4; ++i)
@@ -334,36 +365,56 @@ k_linear(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtens
             }
           }
           if (p.res != nullptr) {
-            const uint4 w = p.vec_res ? ahead.res[g] : *slot;
-            const uint32_t words[4] = {w.x, w.y, w.z, w.w};
+            const uint4 res8 = *slot;
+            const uint32_t words[4] = {res8.x, res8.y, res8.z, res8.w};
 #pragma unroll
             for (int i = 0; i < 4; ++i) v[i] = add2(v[i], unpack2<T>(words[i]));
-            if (more && vec_res && col + kCW < p.N) ahead.res[g] = fetch_res(col + kCW);
           }
           *slot = make_uint4(pack2<T>(v[0].x, v[0].y), pack2<T>(v[1].x, v[1].y),
                              pack2<T>(v[2].x, v[2].y), pack2<T>(v[3].x, v[3].y));
         }
-        const int yhead = col0 / p.yv.cols, yc = col0 - yhead * p.yv.cols;
         if (p.tma_out) {
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) {
-            tma_store_4d(&tmY, out, yc, row0, yhead, b);
+            const int head = tile_col / p.yv.cols;
+            tma_store_4d(&tmY, out + c * 64, col0 - head * p.yv.cols, row0, head, b);
             bulk_commit_group();
           }
-        } else {
-          __syncwarp();
-          T* y = p.y + b * p.yv.batch + yhead * p.yv.head + yc;
-          if (col0 + lane < p.N)
-            for (int rr = 0; rr < 32 && row0 + rr < p.L; ++rr)
-              y[(row0 + rr) * p.yv.row + lane] = *reinterpret_cast<const T*>(
-                  out + rr * kCW * 2 + ((lane / 8) ^ ((rr >> 1) & 3)) * 16 + lane % 8 * 2);
+        }
+        __syncwarp();  // the next chunk's bias goes where this one's was
+      }
+      if (whole && here) {
+        if (!p.tma_out) {
+#pragma unroll 1
+          for (int c = 0; c < C::COLS && tile_col + c < p.N; c += kCW) {
+            const int head = (tile_col + c) / p.yv.cols;
+            T* y = p.y + b * p.yv.batch + head * p.yv.head + row0 * p.yv.row +
+                   (tile_col + c + lane - head * p.yv.cols);
+            const bool in = tile_col + c + lane < p.N;
+#pragma unroll 1
+            for (int r0 = 0; r0 < 32; r0 += 16) {
+              uint16_t words[16];  // all read before the first is stored
+#pragma unroll
+              for (int i = 0; i < 16; ++i) words[i] = *staged(r0 + i, c + lane);
+#pragma unroll
+              for (int i = 0; i < 16; ++i, y += p.yv.row)
+                if (in && row0 + r0 + i < p.L) *reinterpret_cast<uint16_t*>(y) = words[i];
+            }
+          }
+          fence_proxy_async_smem();  // R's next rows are written by TMA
           __syncwarp();
         }
       }
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive_cluster(empty_addr[acc]);
+    }
+    if (!ok && residuals > 0) {  // its copy lands before the CTA ends
+      const uint64_t t0 = globaltimer_ns();
+      while (!mbar_try_wait(&bars.res_full[e], (residuals - 1) & 1) && globaltimer_ns() - t0 < 100000000ull) {
+      }
+      __syncwarp();
     }
     if (lane == 0) bulk_wait_all();
   }
@@ -445,19 +496,20 @@ k_finish(const Params<T> p, int few, int groups, int cols, int rows) {
 // ------------------------------------------------------------------ host side
 template <typename T, int BN, int kAct>
 cudaError_t run_pair(const LinearArgs& a, const Plan& plan, cudaStream_t st) {
-  using C = Cfg<BN>;
   const Params<T> p = params_of<T>(a, plan);
   const int dx = a.K / a.x_heads, dy = a.N / a.y_heads;
-  CUtensorMap tmX, tmW, tmY;
+  CUtensorMap tmX, tmW, tmY, tmR;
   bool ok = map_4d<T>(&tmX, a.X, dx, a.L, a.x_heads, a.Bt, a.xs, kBK, kBM) &&
             map_w<T>(&tmW, a.W, a.K, a.N, a.w_row, BN / 2);
   if (p.tma_out) ok = ok && map_4d<T>(&tmY, a.Y, dy, a.L, a.y_heads, a.Bt, a.ys, kCW, 32);
   else tmY = tmX;
+  if (p.tma_res) ok = ok && map_4d<T>(&tmR, a.R, dy, a.L, a.y_heads, a.Bt, a.rs, kCW, 32);
+  else tmR = tmX;
   if (!ok) return cudaErrorInvalidValue;
   cudaError_t e = cudaFuncSetAttribute(k_linear<T, BN, kAct>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem<T, BN>);
   if (e != cudaSuccess) return e;
-  k_linear<T, BN, kAct><<<2 * plan.groups, C::THREADS, C::SMEM, st>>>(tmX, tmW, tmY, p);
+  k_linear<T, BN, kAct><<<2 * plan.groups, Cfg<BN>::THREADS, kSmem<T, BN>, st>>>(tmX, tmW, tmY, tmR, p);
   return cudaGetLastError();
 }
 

@@ -36,7 +36,8 @@ struct Params {
   T* y;
   View rv, yv;
   int tma_out;          // Y's base and strides allow TMA stores
-  int vec_res;          // R's base and strides allow 16-byte loads
+  int tma_res;          // R's base and strides allow TMA loads
+  int rb, rh;           // 0 where R's batch or head stride is 0
   float* part;          // split sums: [2 groups][rows of a tile][columns of a tile]
   int part_rows;
   int32_t* status;
@@ -202,7 +203,9 @@ Params<T> params_of(const LinearArgs& a, const Plan& plan) {
   p.rv = View{a.rs.batch, a.rs.head, a.rs.row, dy};
   p.yv = View{a.ys.batch, a.ys.head, a.ys.row, dy};
   p.tma_out = whole16(a.Y, a.ys);
-  p.vec_res = a.R != nullptr && a.N % 8 == 0 && whole16(a.R, a.rs);
+  p.tma_res = a.R != nullptr && whole16(a.R, a.rs) && (a.L == 1 || a.rs.row > 0);
+  p.rb = a.rs.batch != 0;
+  p.rh = a.rs.head != 0;
   p.part = align32(a.ws);
   p.part_rows = std::min(a.L, plan.rows);
   p.status = a.status;

@@ -221,3 +221,31 @@ def test_more_than_2_31_outputs():
     y = b.linear(x, w)
     assert not y[0, :L - 300].any()
     _check(y[:, -300:], x[:, -300:], w)
+
+
+# the residual's rows, heads or entries one copy; its base and rows off 16 bytes while the
+# output's are on them, and the other way round
+@pytest.mark.parametrize("L", [300, 4])
+@pytest.mark.parametrize("kind", ["rows", "heads", "entries", "base", "stride", "out"])
+def test_residuals_and_outputs_of_any_stride(L, kind):
+    Bt, K, H, d = 2, 328, 4, 64
+    N = H * d
+    x, w = _randn(Bt, L, K), _randn(N, K, seed=1, scale=K ** -0.5)
+    gate, out = _randn(Bt, N, seed=3), None
+    if kind == "rows":
+        res = _randn(Bt, H, 1, d, seed=4).expand(Bt, H, L, d)
+    elif kind == "heads":
+        res = _randn(Bt, 1, L, d, seed=4).expand(Bt, H, L, d)
+    elif kind == "entries":
+        res = _randn(1, H, L, d, seed=4).expand(Bt, H, L, d)
+    elif kind == "base":
+        res = _randn(Bt * H * L * d + 3, 1, seed=4)[3:].view(Bt, H, L, d)
+    elif kind == "stride":
+        res = _randn(Bt, H, L, d + 5, seed=4)[..., :d]
+    else:
+        res = _randn(Bt, H, L, d, seed=4)
+        out = torch.full((Bt, H, L, d + 2), 9.0, dtype=torch.bfloat16, device=DEV)[..., :d]
+    y = b.linear(x, w, None, b.ACT_SILU, gate, res, heads=H, out=out)
+    _check(y, x, w, None, b.ACT_SILU, gate, res)
+    if out is not None:
+        assert y.data_ptr() == out.data_ptr()
