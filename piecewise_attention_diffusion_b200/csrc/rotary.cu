@@ -37,7 +37,7 @@ struct Params {
   const float* pos;
   int Bt, H, L, n_axes, pos_per_batch, heads_per_cta;
   int groups;  // threads per token: pairs / W
-  int64_t n;   // threads in all: Bt * L * groups
+  int64_t n;   // tokens in all: Bt * L
   float sign;
   // of every pair: turns per unit of position, axis, first and second component
   double rate[kMaxPairs];
@@ -81,8 +81,8 @@ __device__ __forceinline__ Bytes<N> run_of(const float (&f)[N / sizeof(T)]) {
 
 // W pairs per thread. kAdjacent: 2W consecutive components; else W consecutive first
 // components and W consecutive second ones (the host chose W so that neither run crosses
-// a section).
-template <typename T, int W, bool kAdjacent>
+// a section). kAgain: CTAs that fill the SMs go on to further tokens, instead of CTAs for all.
+template <typename T, int W, bool kAdjacent, bool kAgain>
 __global__ void __launch_bounds__(kThreads)
 k_rotary(const __grid_constant__ Params p) {
   // the pair tables, from the parameters (whose reads are serial where lanes differ)
@@ -94,89 +94,108 @@ k_rotary(const __grid_constant__ Params p) {
     axis_s[i] = p.axis[i];
   }
   __syncthreads();
-  const int64_t id = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-  if (id >= p.n) return;
-  const int g = (int)(id % p.groups);
-  const int64_t token = id / p.groups;
-  const int t = (int)(token % p.L), b = (int)(token / p.L);
-  const float* pos = p.pos + ((p.pos_per_batch ? (int64_t)b * p.L : 0) + t) * p.n_axes;
-
-  const int lo = p.lo[g * W], hi = p.hi[g * W];
-  const int h0 = blockIdx.y * p.heads_per_cta;
-  const int h1 = min(h0 + p.heads_per_cta, p.H);
-  const T* x = static_cast<const T*>(p.x) + b * p.xs.batch + t * p.xs.row + h0 * p.xs.head;
-  T* y = static_cast<T*>(p.y) + b * p.ys.batch + t * p.ys.row + h0 * p.ys.head;
-  constexpr int kRun = (int)sizeof(T) * W * (kAdjacent ? 2 : 1);
-
-  // the first heads' components are asked for before the sines are formed
-  Bytes<kRun> first[kUnroll], second[kUnroll];
-  auto fetch = [&](int h) {
-#pragma unroll
-    for (int u = 0; u < kUnroll; ++u)
-      if (h + u < h1) {
-        const T* row = x + u * p.xs.head;
-        first[u] = *reinterpret_cast<const Bytes<kRun>*>(row + lo);
-        if (!kAdjacent) second[u] = *reinterpret_cast<const Bytes<kRun>*>(row + hi);
-      }
-    x += kUnroll * p.xs.head;
-  };
-  fetch(h0);
-
-  float c[W], s[W];
-  bool copy[W];
-#pragma unroll
-  for (int j = 0; j < W; ++j) {
-    const int axis = axis_s[g * W + j];
-    copy[j] = axis == kCopy;
-    c[j] = 1.f;
-    s[j] = 0.f;
-    if (!copy[j]) {
-      double turns = (double)__ldg(pos + axis) * rate_s[g * W + j];
-      turns -= rint(turns);
-      sincospif((float)(2.0 * turns), &s[j], &c[j]);
-      s[j] *= p.sign;
-    }
+  int g;
+  int64_t token;
+  if constexpr (kAgain) {
+    const int per_cta = kThreads / p.groups;
+    if (threadIdx.x >= per_cta * p.groups) return;
+    g = threadIdx.x % p.groups;
+    token = (int64_t)blockIdx.x * per_cta + threadIdx.x / p.groups;
+  } else {
+    const int64_t id = (int64_t)blockIdx.x * kThreads + threadIdx.x;
+    g = (int)(id % p.groups);
+    token = id / p.groups;
   }
-  for (int h = h0; h < h1; h += kUnroll) {
+  do {
+    if (token >= p.n) return;
+    int t, b;
+    if constexpr (kAgain) {
+      b = (uint32_t)token / (uint32_t)p.L;
+      t = (uint32_t)token - b * (uint32_t)p.L;
+    } else {
+      t = (int)(token % p.L);
+      b = (int)(token / p.L);
+    }
+    const float* pos = p.pos + ((p.pos_per_batch ? (int64_t)b * p.L : 0) + t) * p.n_axes;
+
+    const int lo = p.lo[g * W], hi = p.hi[g * W];
+    const int h0 = blockIdx.y * p.heads_per_cta;
+    const int h1 = min(h0 + p.heads_per_cta, p.H);
+    const T* x = static_cast<const T*>(p.x) + b * p.xs.batch + t * p.xs.row + h0 * p.xs.head;
+    T* y = static_cast<T*>(p.y) + b * p.ys.batch + t * p.ys.row + h0 * p.ys.head;
+    constexpr int kRun = (int)sizeof(T) * W * (kAdjacent ? 2 : 1);
+
+    // the first heads' components are asked for before the sines are formed
+    Bytes<kRun> first[kUnroll], second[kUnroll];
+    auto fetch = [&](int h) {
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u)
-      if (h + u < h1) {
-        T* row = y + u * p.ys.head;
-        if constexpr (kAdjacent) {
-          float f[2 * W];
+      for (int u = 0; u < kUnroll; ++u)
+        if (h + u < h1) {
+          const T* row = x + u * p.xs.head;
+          first[u] = *reinterpret_cast<const Bytes<kRun>*>(row + lo);
+          if (!kAdjacent) second[u] = *reinterpret_cast<const Bytes<kRun>*>(row + hi);
+        }
+      x += kUnroll * p.xs.head;
+    };
+    fetch(h0);
+
+    float c[W], s[W];
+    bool copy[W];
 #pragma unroll
-          for (int j = 0; j < W; ++j) {
-            const float xa = element<T>(first[u], 2 * j), xb = element<T>(first[u], 2 * j + 1);
-            f[2 * j] = xa * c[j] - xb * s[j];
-            f[2 * j + 1] = xa * s[j] + xb * c[j];
-          }
-          Bytes<kRun> out = run_of<T, kRun>(f);
-          // copied components are taken bit for bit: an infinity, a NaN stays as it is
-          constexpr int kPairWords = (int)sizeof(T) / 2;
+    for (int j = 0; j < W; ++j) {
+      const int axis = axis_s[g * W + j];
+      copy[j] = axis == kCopy;
+      c[j] = 1.f;
+      s[j] = 0.f;
+      if (!copy[j]) {
+        double turns = (double)__ldg(pos + axis) * rate_s[g * W + j];
+        turns -= rint(turns);
+        sincospif((float)(2.0 * turns), &s[j], &c[j]);
+        s[j] *= p.sign;
+      }
+    }
+    for (int h = h0; h < h1; h += kUnroll) {
 #pragma unroll
-          for (int i = 0; i < kRun / 4; ++i)
-            if (copy[i / kPairWords]) out.w[i] = first[u].w[i];
-          *reinterpret_cast<Bytes<kRun>*>(row + lo) = out;
-        } else {
-          // the run lies in one section: turned or copied as a whole
-          if (!copy[0]) {
-            float f[W], d[W];
+      for (int u = 0; u < kUnroll; ++u)
+        if (h + u < h1) {
+          T* row = y + u * p.ys.head;
+          if constexpr (kAdjacent) {
+            float f[2 * W];
 #pragma unroll
             for (int j = 0; j < W; ++j) {
-              const float xa = element<T>(first[u], j), xb = element<T>(second[u], j);
-              f[j] = xa * c[j] - xb * s[j];
-              d[j] = xa * s[j] + xb * c[j];
+              const float xa = element<T>(first[u], 2 * j), xb = element<T>(first[u], 2 * j + 1);
+              f[2 * j] = xa * c[j] - xb * s[j];
+              f[2 * j + 1] = xa * s[j] + xb * c[j];
             }
-            first[u] = run_of<T, kRun>(f);
-            second[u] = run_of<T, kRun>(d);
+            Bytes<kRun> out = run_of<T, kRun>(f);
+            // copied components are taken bit for bit: an infinity, a NaN stays as it is
+            constexpr int kPairWords = (int)sizeof(T) / 2;
+#pragma unroll
+            for (int i = 0; i < kRun / 4; ++i)
+              if (copy[i / kPairWords]) out.w[i] = first[u].w[i];
+            *reinterpret_cast<Bytes<kRun>*>(row + lo) = out;
+          } else {
+            // the run lies in one section: turned or copied as a whole
+            if (!copy[0]) {
+              float f[W], d[W];
+#pragma unroll
+              for (int j = 0; j < W; ++j) {
+                const float xa = element<T>(first[u], j), xb = element<T>(second[u], j);
+                f[j] = xa * c[j] - xb * s[j];
+                d[j] = xa * s[j] + xb * c[j];
+              }
+              first[u] = run_of<T, kRun>(f);
+              second[u] = run_of<T, kRun>(d);
+            }
+            *reinterpret_cast<Bytes<kRun>*>(row + lo) = first[u];
+            *reinterpret_cast<Bytes<kRun>*>(row + hi) = second[u];
           }
-          *reinterpret_cast<Bytes<kRun>*>(row + lo) = first[u];
-          *reinterpret_cast<Bytes<kRun>*>(row + hi) = second[u];
         }
-      }
-    y += kUnroll * p.ys.head;
-    fetch(h + kUnroll);
-  }
+      y += kUnroll * p.ys.head;
+      fetch(h + kUnroll);
+    }
+    if constexpr (kAgain) token += (int64_t)gridDim.x * (kThreads / p.groups);
+  } while (kAgain);
 }
 
 template <typename T, int W, bool kAdjacent>
@@ -184,15 +203,21 @@ cudaError_t run(Params& p, cudaStream_t st) {
   int pairs = 0;
   while (pairs < kMaxPairs && p.axis[pairs] != 254) ++pairs;
   p.groups = pairs / W;
-  p.n = (int64_t)p.Bt * p.L * p.groups;
-  const int64_t ctas = (p.n + kThreads - 1) / kThreads;
+  p.n = (int64_t)p.Bt * p.L;
+  const int64_t ctas = (p.n * p.groups + kThreads - 1) / kThreads;
   // all heads in one thread share its sines; fewer per thread where that leaves the card
   // short of CTAs
   const int64_t want = 148 * 8;
   int split = (int)std::min<int64_t>(ceil_div(p.H, kUnroll), (want + ctas - 1) / ctas);
   p.heads_per_cta = ceil_div(ceil_div(p.H, split), kUnroll) * kUnroll;
-  const dim3 grid((unsigned)ctas, (unsigned)ceil_div(p.H, p.heads_per_cta));
-  k_rotary<T, W, kAdjacent><<<grid, kThreads, 0, st>>>(p);
+  const unsigned heads = (unsigned)ceil_div(p.H, p.heads_per_cta);
+  // A thread with one pair of few heads ends before its CTA's tables have paid. bf16, halves paired,
+  // odd sections of 128, 4 entries: 3 heads x 30323 tokens 89 us, 172 with CTAs for all; 16 x 12000
+  // 99, 105.
+  if (W == 1 && p.heads_per_cta <= 4 * kUnroll && ctas > 16 * 148)
+    k_rotary<T, W, kAdjacent, W == 1><<<dim3(16 * 148, heads), kThreads, 0, st>>>(p);
+  else
+    k_rotary<T, W, kAdjacent, false><<<dim3((unsigned)ctas, heads), kThreads, 0, st>>>(p);
   return cudaGetLastError();
 }
 
