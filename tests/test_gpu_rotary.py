@@ -192,3 +192,17 @@ def test_more_than_2_31_elements():
     b.rotary(x, pos, (128,), out=x)
     assert torch.equal(x[:, 127:, -3:], want)
     assert not x[0, 126, -1].any()
+
+
+# CTAs that go on to further tokens: few heads, sections with odd halves, entries that end inside
+# a CTA's tokens; threads per token that divide the CTA's, and that do not
+@pytest.mark.parametrize("H,d,axes", [(3, 40, (2, 36)), (1, 64, (18, 46)), (13, 40, (38,))])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_few_heads_of_many_tokens(H, d, axes, dtype):
+    Bt, L = 3, 13001
+    x = _x((Bt, H, L, d), dtype, rows=True)
+    pos = _pos(L, len(axes), Bt)
+    y = b.rotary(x, pos, axes, pairing=b.PAIR_HALVES, inverse=True)
+    _check(y, x, pos, axes, True, True)
+    one = _pos(L, len(axes), seed=2)
+    _check(b.rotary(x, one, axes, pairing=b.PAIR_HALVES), x, one, axes, True)
