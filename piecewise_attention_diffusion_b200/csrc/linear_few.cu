@@ -167,7 +167,7 @@ k_linear_few(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CU
       const bool whole = !partial(p, w), in = col < p.N;
       const float bias = whole && in && p.bias != nullptr ? to_f32(p.bias[col]) : 0.f;
       const int rhead = col / p.rv.cols, yhead = col / p.yv.cols;
-      const T* res = p.res + b * p.rv.batch + rhead * p.rv.head + (col - rhead * p.rv.cols);
+      const T* at_res = p.res + b * p.rv.batch + rhead * p.rv.head + (col - rhead * p.rv.cols);
       T* y = p.y + b * p.yv.batch + yhead * p.yv.head + (col - yhead * p.yv.cols);
       float* part = whole ? nullptr : slot_of(p, w, group, kCols) + c;
       ok = mbar_wait(&bars.acc_full[acc], (it / 2) & 1, abort_flag, p.wait_ns);
@@ -176,6 +176,28 @@ k_linear_few(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CU
       tc_fence_after();
 #pragma unroll 1
       for (int m0 = 0; m0 < R && m0 < p.L; m0 += 16) {
+        // residuals and gates of 16 rows, all asked for before the first is used
+        T res[16], gate[16];
+        const bool use = whole && in;
+        if (use && p.res != nullptr) {
+          const T* at = at_res + m0 * p.rv.row;
+#pragma unroll
+          for (int i = 0; i < 16; ++i, at += p.rv.row)
+            if (m0 + i < p.L) res[i] = *at;
+        }
+        if (use && p.gate != nullptr) {
+          const int first = (b * p.L + m0) / p.gate_rows;
+          const T* at = p.gate + (int64_t)first * p.N + col;
+          int left = p.gate_rows - (b * p.L + m0 - first * p.gate_rows);  // rows of this vector
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            if (m0 + i < p.L) gate[i] = *at;
+            if (--left == 0) {
+              at += p.N;
+              left = p.gate_rows;
+            }
+          }
+        }
         uint32_t r[16];
         tmem_ld16(tmem + ((uint32_t)(quad * 32) << 16) + acc * R + m0, r);
         tmem_wait_ld();
@@ -186,15 +208,15 @@ k_linear_few(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CU
           continue;
         }
         if (!in) continue;
+        T* at = y + m0 * p.yv.row;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const int row = m0 + i;
-          if (row >= p.L) break;
+        for (int i = 0; i < 16; ++i, at += p.yv.row) {
+          if (m0 + i >= p.L) break;
           float z = __uint_as_float(r[i]) + bias;
           z = activate<kAct>(make_float2(z, z)).x;
-          if (p.gate != nullptr) z *= to_f32(p.gate[(int64_t)((b * p.L + row) / p.gate_rows) * p.N + col]);
-          if (p.res != nullptr) z += to_f32(res[row * p.rv.row]);
-          y[row * p.yv.row] = from_f32<T>(z);
+          if (p.gate != nullptr) z *= to_f32(gate[i]);
+          if (p.res != nullptr) z += to_f32(res[i]);
+          *at = from_f32<T>(z);
         }
       }
       tc_fence_before();
