@@ -820,6 +820,8 @@ struct Plan {
   bool few;
   int parts, ctas;
 };
+// see plan_of; the bytes are those of a row's part in fp32, between d = 64 and 128
+constexpr double kTileUs = 1.3, kItemUs = 2.5, kJoinUs = 4.0, kPartBytes = 400;
 Plan plan_of(int Bt, int H, int Hkv, int Lq, int Lk) {
   const int sms = fwdtiles::sm_count();
   if (Lk > 0 && (int64_t)H / Hkv * Lq <= kMostRows) {
@@ -841,13 +843,26 @@ Plan plan_of(int Bt, int H, int Hkv, int Lq, int Lk) {
     }
     return best;
   }
-  // runs of key tiles per row tile: as many as fill the SMs, none below four tiles
+  // Runs of key tiles per row tile, four tiles each at least: those that make the SMs' longest
+  // time least, in us from measured times of a tile, of an item beside its tiles, and of the join
+  // of the parts (and their bytes, written and read). 6 x 16 heads x 28 queries x 5870 keys x 64,
+  // masked: 75 us in 3 runs, 97 in one; 4 x 16 x 385 x 8741: one run, 109.
   const int64_t items = (int64_t)Bt * H * ceil_div(Lq, 2 * kBQ);
-  const int tiles = ceil_div(Lk, kBK);
-  const int64_t want = sms / items;
-  if (want < 2 || tiles < 8) return Plan{false, 1, 0};
-  const int per = ceil_div(tiles, (int)std::min<int64_t>(want, tiles / 4));
-  return Plan{false, ceil_div(tiles, per), 0};
+  const int tiles = std::max(1, ceil_div(Lk, kBK));
+  const double joined = 2.0 * Bt * H * Lq * kPartBytes / 5e6;
+  Plan best{false, 1, 0};
+  double cost = 1e300;
+  for (int s = 1; s <= std::max(1, tiles / 4) && s <= sms; ++s) {
+    const int per = ceil_div(tiles, s);
+    if (ceil_div(tiles, per) != s) continue;  // the same runs with a part less
+    const double c = (double)((items * s + sms - 1) / sms) * (kTileUs * per + kItemUs) +
+                     (s > 1 ? kJoinUs + s * joined : 0.0);
+    if (c < cost) {
+      cost = c;
+      best.parts = s;
+    }
+  }
+  return best;
 }
 
 Shares shares_of(const CrossArgs& a, const Plan& plan) {
