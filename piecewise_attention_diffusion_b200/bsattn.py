@@ -3,8 +3,9 @@
 Argument marshalling only: every step of the computation runs in the library's CUDA
 kernels. torch supplies device memory and the current stream. The functions named
 ``bsa_*`` mirror the C entry points one to one and take torch tensors; the lower-case
-helpers (``build_mask``, ``precompute``, ``route``, ``forward``) allocate the outputs
-and workspace with torch and call them.
+helpers (``build_mask``, ``precompute``, ``route``, ``forward``; around the block attention
+``rotary``, ``linear``, ``cross_forward``) allocate the outputs and workspace with torch and
+call them.
 
 If the shared library is missing or cannot be loaded, every call raises: there is no
 fallback implementation.
