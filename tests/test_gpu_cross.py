@@ -333,3 +333,19 @@ def test_query_heads_of_one_key_head(Lq, layout):
         o = room if out == "heads" else room.transpose(1, 2)
         o, lse = b.cross_forward(q, k, v, key_len=n, want_lse=True, out=o)
         _check(o, lse, q, k, v, key_len=n)
+
+
+# heads and masks together where heads are folded, and long runs of keys joined from many parts
+@pytest.mark.parametrize("size", [(2, 8, 2, 1, 3001, 128), (1, 8, 1, 33, 2500, 64),
+                                  (3, 6, 2, 1, 900, 64), (1, 1, 1, 1, 70000, 64),
+                                  (2, 40, 8, 1, 2049, 128)])
+def test_folded_heads_under_masks_and_counts(size):
+    Bt, H, Hkv, Lq, Lk, d = size
+    q = _randn(Bt, H, Lq, d, dtype=torch.float16)
+    k, v = (_randn(Bt, Hkv, Lk, d, dtype=torch.float16, seed=s) for s in (1, 2))
+    g = torch.Generator().manual_seed(3)
+    mask = (torch.rand(Bt, Lk, generator=g) < 0.7).to(torch.uint8).to(DEV)
+    n = torch.tensor([Lk - 3, Lk // 3, 0][:Bt], dtype=torch.int32, device=DEV)
+    _spoil(k, v, n, mask)
+    o, lse = b.cross_forward(q, k, v, key_len=n, key_mask=mask, want_lse=True)
+    _check(o, lse, q, k, v, key_len=n, key_mask=mask)

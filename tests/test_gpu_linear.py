@@ -249,3 +249,15 @@ def test_residuals_and_outputs_of_any_stride(L, kind):
     _check(y, x, w, None, b.ACT_SILU, gate, res)
     if out is not None:
         assert y.data_ptr() == out.data_ptr()
+
+
+@pytest.mark.parametrize("L", [300, 4])
+@pytest.mark.parametrize("step", [8, 16, 3])
+def test_a_residual_whose_rows_overlap(L, step):
+    """A window that moves by fewer elements than it is wide: rows are only read."""
+    N, K = 192, 136
+    x, w = _randn(1, L, K), _randn(N, K, seed=1, scale=K ** -0.5)
+    res = _randn(L * step + N, 1, seed=4).as_strided((1, L, N), (0, step, 1))
+    _check(b.linear(x, w, residual=res), x, w, residual=res)
+    xs = _randn(L * 8 + K, 1, seed=5).as_strided((1, L, K), (0, 8, 1))
+    _check(b.linear(xs, w), xs, w)
