@@ -109,6 +109,22 @@ __device__ __forceinline__ float2 mul2(float2 a, float2 b) {
   return fma2(a, b, make_float2(-0.f, -0.f));
 }
 
+// 1 - Phi(a) = e^(-a^2 / 2) t Q(t), t = 1 / (1 + kTailP a), for a >= 0: t Q(t) is half the scaled
+// complementary error function, Q of degree 6 with the least relative error, 6.3e-7 (a linear
+// program over t). With fp32's rounding the product z Phi(z) is off by 5.3e-7 |z|.
+constexpr float kTailP = 0.26516503f;
+__device__ __forceinline__ float2 normal_tail(float2 a) {
+  constexpr float kTail[7] = {0.105669923f, 0.107841954f, 0.0833459124f, 0.141495913f,
+                              -0.0647517219f, 0.193937004f, -0.0675393045f};
+  const float2 t = make_float2(__fdividef(1.0f, fmaf(a.x, kTailP, 1.0f)),
+                               __fdividef(1.0f, fmaf(a.y, kTailP, 1.0f)));
+  float2 q = make_float2(kTail[6], kTail[6]);
+#pragma unroll
+  for (int i = 5; i >= 0; --i) q = fma2(q, t, make_float2(kTail[i], kTail[i]));
+  const float2 x = mul2(mul2(a, a), make_float2(-0.72134752f, -0.72134752f));  // -log2(e) / 2
+  return mul2(mul2(q, t), make_float2(ex2(x.x), ex2(x.y)));
+}
+
 // The activation is a template argument: with a branch per element nothing overlapped, and
 // the epilogue of a 128 x 256 tile took 40000 cycles where its products take 8300 (K = 1024).
 template <int kAct>
@@ -119,9 +135,10 @@ __device__ __forceinline__ float2 activate(float2 z) {
     const float2 t = fma2(mul2(z, z), make_float2(d, d), make_float2(c, c));
     return sigmoid_times(z, mul2(z, t));
   }
-  if (kAct == BSA_ACT_GELU_ERF)  // the complementary form keeps the tail of negative z
-    return make_float2(0.5f * z.x * erfcf(-0.70710678118654752f * z.x),
-                       0.5f * z.y * erfcf(-0.70710678118654752f * z.y));
+  if (kAct == BSA_ACT_GELU_ERF) {  // z Phi(z) by the normal tail, which keeps negative z's digits
+    const float2 h = normal_tail(make_float2(fabsf(z.x), fabsf(z.y)));
+    return make_float2(z.x * (z.x < 0.f ? h.x : 1.0f - h.x), z.y * (z.y < 0.f ? h.y : 1.0f - h.y));
+  }
   if (kAct == BSA_ACT_SILU) return sigmoid_times(z, mul2(z, make_float2(kLog2e, kLog2e)));
   return z;
 }
