@@ -21,7 +21,9 @@
 //           (infinities, NaN) meets no product;
 //   warp 10 clears those rows of K where there is a key mask: their scores are then known to be
 //           0, and their share of the sum is taken off as a whole, instead of a select per score
-//           in every tile (292 against 347 us, 2 x 16 heads x 4101 queries x 4352 keys).
+//           in every tile (292 against 347 us, 2 x 16 heads x 4101 queries x 4352 keys). It also
+//           leaves the softmax which keys those are. Four rows at a time, a bit per row: 298 us
+//           where row by row took 309; 5 x 40 heads x 48 x 3 keys 11.7, 16.5.
 // TMEM: S0 [0,128), S1 [128,256), O0 [256, 256 + D), O1 [256 + D, 256 + 2 D); P overlays S.
 // Few rows: the keys are split into runs that separate items take; each leaves its O, m and l
 // in the workspace, and k_join adds them in order. Query heads that share a key head are taken
@@ -247,6 +249,12 @@ k_cross(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtenso
   __shared__ Barriers bars;
   __shared__ uint32_t tmem_base_sh;
   __shared__ int abort_sh;
+  // Of a tile of K, with a key mask, the keys that are not real and their number, by the warp that
+  // clears them. It is at most NK + 1 tiles ahead of a softmax that reads them.
+  constexpr uint32_t kOutRing = 8;
+  static_assert(C::NK + 1 < kOutRing, "a tile's entry is read before it is written again");
+  __shared__ uint8_t out_sh[kOutRing][32];
+  __shared__ uint32_t gone_sh[kOutRing];
 
   // k_join may take its place now; it waits for this grid before it reads a run
   if (p.splits > 1) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -491,31 +499,43 @@ k_cross(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtenso
           const uint32_t out = next;
           if (kKeyMask) next = excluded(p, it, t + 1, lane);
           const uint32_t slot = n % ring;
+          if (kKeyMask && is_k) {
+            // for the softmax: this lane's keys, and how many are not real: all, and those whose
+            // exponentials go to the FMA pipe (keys 0 to 3 of every 16: lanes 0, 4, 8, ...)
+            const uint32_t own = __popc(out);
+            const uint32_t gone = __reduce_add_sync(0xffffffffu, own + (lane % 4 == 0 ? own << 16 : 0u));
+            out_sh[n % kOutRing][lane] = (uint8_t)out;
+            if (lane == 0) gone_sh[n % kOutRing] = gone;
+          }
           ok = mbar_wait_warp(&full[slot], (n / ring) & 1, abort_flag, p.wait_ns);
           if (!ok) break;
           if (tile_masked(p, it, t)) {
-            // A row is 128 bytes in each of the D / 64 sub-tiles: D / 8 lanes clear it, the warp
-            // 32 / (D / 8) rows at a time.
-            constexpr int kPieces = D / 8, kRows = 32 / kPieces;
-            unsigned char* at = (is_k ? sK : sV) + slot * C::SLOT +
-                                (lane % kPieces / 8) * (kBK * 128) + (lane % 8) * 16;
-            const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+            // A row is 128 bytes in each of the D / 64 sub-tiles. Eight lanes clear it, the warp
+            // four rows at a time; rows behind the last key are zeros as they come.
+            const int inside = min(kBK, p.Lk - (it.t0 + t) * kBK);
+            uint32_t rows = 0;  // bit i: row 4 i + lane / 8
             if (!kKeyMask) {
-              for (int k = it.len - (it.t0 + t) * kBK + lane / kPieces; k < kBK; k += kRows)
-                *reinterpret_cast<uint4*>(at + k * 128) = zero;
-            } else {  // bit i of word j: key 4 i + j
+              const int from = it.len - (it.t0 + t) * kBK;
+              for (int i = 0; i < kBK / 4; ++i) {
+                const int row = 4 * i + lane / 8;
+                if (row >= from && row < inside) rows |= 1u << i;
+              }
+            } else {
+              const int mine = max(0, min(4, inside - 4 * lane));
+              const uint32_t there = out & ((1u << mine) - 1u);
 #pragma unroll
-              for (int j = 0; j < 4; ++j)
-                for (uint32_t w = __ballot_sync(0xffffffffu, (out >> j) & 1u); w != 0;) {
-                  int k = -1;
-#pragma unroll
-                  for (int r = 0; r < kRows; ++r) {
-                    if (r == lane / kPieces && w != 0) k = 4 * (__ffs(w) - 1) + j;
-                    w &= w - 1;
-                  }
-                  if (k >= 0) *reinterpret_cast<uint4*>(at + k * 128) = zero;
-                }
+              for (int j = 0; j < 4; ++j) {
+                const uint32_t word = __ballot_sync(0xffffffffu, (there >> j) & 1u);
+                if (lane / 8 == j) rows = word;
+              }
             }
+            unsigned char* at = (is_k ? sK : sV) + slot * C::SLOT + lane * 16;
+#pragma unroll
+            for (int i = 0; i < kBK / 4; ++i)
+              if ((rows >> i) & 1u)
+#pragma unroll
+                for (int h = 0; h < D / 64; ++h)
+                  *reinterpret_cast<uint4*>(at + h * (kBK * 128) + i * 512) = make_uint4(0u, 0u, 0u, 0u);
             fence_proxy_async_smem();
           }
           mbar_arrive(&cleared[slot]);
@@ -533,22 +553,15 @@ k_cross(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtenso
     const uint32_t s_base = tmem + lane_addr + C::S_COL(x);
     const uint32_t o_base = tmem + lane_addr + C::O_COL(x);
     unsigned char* out = sV + C::NV * C::SLOT + warp * C::OUT;
-    uint32_t tiles = 0, finals = 0;
+    uint32_t tiles = 0, finals = 0, all = 0;
     bool ok = true;
     for (int i = blockIdx.x; i < p.n_items; i += gridDim.x) {
       const Item it = item_of(p, i);
+      const uint32_t first = all;  // of the item's tiles, in the count of the K ring
+      all += it.n;
       if (x == 1 && !it.two) continue;
       float m_run = -INFINITY, l = 0.f;
       for (int t = 0; t < it.n; ++t) {
-        const bool masked = tile_masked(p, it, t);
-        // with a key mask, how many of the tile's keys are not real: all, and those whose
-        // exponentials go to the FMA pipe (keys 0 to 3 of every 16: lanes 0, 4, 8, ...)
-        uint32_t out = 0, gone = 0;
-        if (kKeyMask && masked) {
-          out = excluded(p, it, t, lane);
-          const uint32_t own = __popc(out);
-          gone = __reduce_add_sync(0xffffffffu, own + (lane % 4 == 0 ? own << 16 : 0u));
-        }
         ok = mbar_wait(&bars.s_full[x], tiles & 1, abort_flag, p.wait_ns);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
@@ -561,9 +574,10 @@ k_cross(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtenso
         tmem_ld32(s_base + 96, *reinterpret_cast<uint32_t(*)[32]>(r + 96));
         tmem_wait_ld();
         bool surplus = false;
+        uint32_t gone = 0;
         float mx;
         if (!kKeyMask) {
-          if (masked) {
+          if (tile_masked(p, it, t)) {
             const int real = it.len - (it.t0 + t) * kBK;
 #pragma unroll
             for (int w = 0; w < 4; ++w) {
@@ -581,6 +595,7 @@ k_cross(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtenso
           // beside the sum (which is at least 1), it is taken off again below; V's rows are zeros,
           // so O needs nothing. Else they are replaced by -inf, at three instructions a score.
           mx = row_max(r) * p.scale_log2;
+          gone = gone_sh[(first + t) % kOutRing];
           if (gone != 0) {
             const bool grows = mx > m_run + kRescaleLog2;
             const float ref = grows ? mx : m_run;
@@ -588,6 +603,7 @@ k_cross(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtenso
             surplus = __all_sync(0xffffffffu, (grows ? mx > 0.f : m_run >= 0.f) && extra <= 8.f);
           }
           if (gone != 0 && !surplus) {
+            const uint32_t out = out_sh[(first + t) % kOutRing][lane];
 #pragma unroll
             for (int w = 0; w < 4; ++w) {
               const uint32_t word = __reduce_or_sync(
