@@ -19,12 +19,13 @@
 //              gate and residual in fp32, one rounding, back into the buffer, and a TMA store.
 //              (Where strides rule TMA out: coalesced 2-byte accesses, 16 rows at a time.) Two
 //              TMEM accumulators, so the epilogue of one tile runs under the products of the next.
-// Measured out of L2, bf16: 16384 x 5120 x 5120 with bias, gate and residual 588-690 us (by the
-// power limit; 1.25-1.46 PFLOP/s), the tensor pipe at 93%; 9216 x 1024 x 4096 with GELU 66 us,
+// Measured out of L2, bf16: 16384 x 5120 x 5120 with bias, gate and residual 556-690 us (by the
+// power limit; 1.25-1.55 PFLOP/s), the tensor pipe at 93%; 9216 x 1024 x 4096 with GELU 66 us,
 // bound by the epilogue, whose warps wait on one latency after the other; 23240 x 400 x 2560 with
-// GELU (erf), gate and residual 109 us (177 with the library's erfcf); 2928 x 168 x 19968 with a residual 83 us where 16-byte loads of it by the lanes
-// that own its rows took 126. Chunks are 32 columns because boxes of 64 (128-byte rows), stored
-// once per tile, delay the operands' loads: 2.3% more time at K = 5120.
+// GELU (erf), gate and residual 109 us (177 with CUDA's erfcf); 2928 x 168 x 19968 with a residual
+// 83 us where 16-byte loads of it by the lanes that own its rows took 126. Chunks are 32 columns
+// because boxes of 64 (128-byte rows), stored once per tile, delay the operands' loads: 2.3% more
+// time at K = 5120.
 // Every mbarrier wait is bounded; on a timeout the pair drains, frees TMEM and reports
 // BSA_ERR_TIMEOUT.
 #include <algorithm>
