@@ -19,11 +19,14 @@
 //   warp 9  MMA issuer: S(t) = Q K(t)^T, O += P(t) V(t) with P as the TMEM operand;
 //   warp 11  clears the rows of V that key counts and masks exclude, so that what lies there
 //           (infinities, NaN) meets no product;
-//   warp 10 clears those rows of K where there is a key mask: their scores are then known to be
-//           0, and their share of the sum is taken off as a whole, instead of a select per score
-//           in every tile (292 against 347 us, 2 x 16 heads x 4101 queries x 4352 keys). It also
-//           leaves the softmax which keys those are. Four rows at a time, a bit per row: 298 us
-//           where row by row took 309; 5 x 40 heads x 48 x 3 keys 11.7, 16.5.
+//   warp 10 clears those rows of K where there is a key mask, so that their scores are 0, and
+//           leaves the softmax a term per key, 0 or -inf, which is added to the scores: two keys
+//           an instruction, where a select per score took three instructions a key (2 x 16 heads x
+//           4101 queries x 4352 keys, a fifth masked: 287 us whatever the scores; 325 with the
+//           select). To let the zeros through and take their exponentials off the sum again took
+//           278 us where the scores allowed it, but what rounding left of them grew with the
+//           number of tiles: 2.7e-4 of a sum after 256. Rows are cleared four at a time, a bit
+//           per row; row by row took 4% more.
 // TMEM: S0 [0,128), S1 [128,256), O0 [256, 256 + D), O1 [256 + D, 256 + 2 D); P overlays S.
 // Few rows: the keys are split into runs that separate items take; each leaves its O, m and l
 // in the workspace, and k_join adds them in order. Query heads that share a key head are taken
@@ -249,12 +252,13 @@ k_cross(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtenso
   __shared__ Barriers bars;
   __shared__ uint32_t tmem_base_sh;
   __shared__ int abort_sh;
-  // Of a tile of K, with a key mask, the keys that are not real and their number, by the warp that
-  // clears them. It is at most NK + 1 tiles ahead of a softmax that reads them.
-  constexpr uint32_t kOutRing = 8;
-  static_assert(C::NK + 1 < kOutRing, "a tile's entry is read before it is written again");
-  __shared__ uint8_t out_sh[kOutRing][32];
-  __shared__ uint32_t gone_sh[kOutRing];
+  // With a key mask, of a tile of K: what is added to the scores (0, or -inf where a key is not
+  // real), and how many keys are not real. The warp that clears K's rows writes them once the tile
+  // is there: then the scores of the tile NK before it are computed, so that no softmax reads one
+  // further back, and NK + 1 entries do.
+  constexpr uint32_t kTermRing = kKeyMask ? C::NK + 1 : 1;
+  __shared__ __align__(16) float term_sh[kTermRing][kBK];
+  __shared__ uint32_t gone_sh[kTermRing];
 
   // k_join may take its place now; it waits for this grid before it reads a run
   if (p.splits > 1) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -499,16 +503,15 @@ k_cross(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtenso
           const uint32_t out = next;
           if (kKeyMask) next = excluded(p, it, t + 1, lane);
           const uint32_t slot = n % ring;
-          if (kKeyMask && is_k) {
-            // for the softmax: this lane's keys, and how many are not real: all, and those whose
-            // exponentials go to the FMA pipe (keys 0 to 3 of every 16: lanes 0, 4, 8, ...)
-            const uint32_t own = __popc(out);
-            const uint32_t gone = __reduce_add_sync(0xffffffffu, own + (lane % 4 == 0 ? own << 16 : 0u));
-            out_sh[n % kOutRing][lane] = (uint8_t)out;
-            if (lane == 0) gone_sh[n % kOutRing] = gone;
-          }
           ok = mbar_wait_warp(&full[slot], (n / ring) & 1, abort_flag, p.wait_ns);
           if (!ok) break;
+          if (kKeyMask && is_k) {  // for the softmax
+            const uint32_t gone = __reduce_add_sync(0xffffffffu, __popc(out));
+            auto term = [&](int j) { return (out >> j) & 1u ? -INFINITY : 0.f; };
+            reinterpret_cast<float4*>(term_sh[n % kTermRing])[lane] =
+                make_float4(term(0), term(1), term(2), term(3));
+            if (lane == 0) gone_sh[n % kTermRing] = gone;
+          }
           if (tile_masked(p, it, t)) {
             // A row is 128 bytes in each of the D / 64 sub-tiles. Eight lanes clear it, the warp
             // four rows at a time; rows behind the last key are zeros as they come.
@@ -573,9 +576,8 @@ k_cross(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtenso
         tmem_ld32(s_base + 64, *reinterpret_cast<uint32_t(*)[32]>(r + 64));
         tmem_ld32(s_base + 96, *reinterpret_cast<uint32_t(*)[32]>(r + 96));
         tmem_wait_ld();
-        bool surplus = false;
-        uint32_t gone = 0;
-        float mx;
+        const uint32_t entry = (first + t) % kTermRing;
+        bool gone = false;
         if (!kKeyMask) {
           if (tile_masked(p, it, t)) {
             const int real = it.len - (it.t0 + t) * kBK;
@@ -588,32 +590,31 @@ k_cross(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtenso
                 if ((word >> e) & 1u) r[32 * w + e] = __float_as_uint(-INFINITY);
             }
           }
-          mx = row_max(r) * p.scale_log2;
         } else {
-          // The scores of keys that are not real are 0 (their rows of K are zeros). Where that
-          // cannot have set the row's reference, and where what they add to the sum is small
-          // beside the sum (which is at least 1), it is taken off again below; V's rows are zeros,
-          // so O needs nothing. Else they are replaced by -inf, at three instructions a score.
-          mx = row_max(r) * p.scale_log2;
-          gone = gone_sh[(first + t) % kOutRing];
-          if (gone != 0) {
-            const bool grows = mx > m_run + kRescaleLog2;
-            const float ref = grows ? mx : m_run;
-            const float extra = (float)(gone & 0xffffu) * ex2(-ref);
-            surplus = __all_sync(0xffffffffu, (grows ? mx > 0.f : m_run >= 0.f) && extra <= 8.f);
-          }
-          if (gone != 0 && !surplus) {
-            const uint32_t out = out_sh[(first + t) % kOutRing][lane];
+          gone = gone_sh[entry] != 0;
+          if (gone) {
+            const float4* term = reinterpret_cast<const float4*>(term_sh[entry]);
 #pragma unroll
-            for (int w = 0; w < 4; ++w) {
-              const uint32_t word = __reduce_or_sync(
-                  0xffffffffu, lane / 8 == w ? out << (lane % 8 * 4) : 0u);
-#pragma unroll
-              for (int e = 0; e < 32; ++e)
-                if ((word >> e) & 1u) r[32 * w + e] = __float_as_uint(-INFINITY);
+            for (int e = 0; e < kBK; e += 4) {
+              const float4 u = term[e / 4];
+              const float2 a = add2(make_float2(__uint_as_float(r[e]), __uint_as_float(r[e + 1])),
+                                    make_float2(u.x, u.y));
+              const float2 b = add2(make_float2(__uint_as_float(r[e + 2]), __uint_as_float(r[e + 3])),
+                                    make_float2(u.z, u.w));
+              r[e] = __float_as_uint(a.x);
+              r[e + 1] = __float_as_uint(a.y);
+              r[e + 2] = __float_as_uint(b.x);
+              r[e + 3] = __float_as_uint(b.y);
             }
-            mx = row_max(r) * p.scale_log2;
           }
+        }
+        float mx = row_max(r) * p.scale_log2;
+        if (kKeyMask && gone && __any_sync(0xffffffffu, mx != mx)) {
+          // a query that is not finite: its products with the zeros are NaN, and so the sums
+#pragma unroll
+          for (int e = 0; e < kBK; ++e)
+            if (term_sh[entry][e] != 0.f) r[e] = __float_as_uint(-INFINITY);
+          mx = row_max(r) * p.scale_log2;
         }
         const bool need = mx > m_run + kRescaleLog2;
         if (__any_sync(0xffffffffu, need)) {
@@ -641,11 +642,6 @@ k_cross(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtenso
           l += row_exp<T, 0>(r, p.scale_log2, m_ref, s_base, &bars.p_half[x]);
         else
           l += row_exp<T, kPolyOf8>(r, p.scale_log2, m_ref, s_base, &bars.p_half[x]);
-        if (kKeyMask && surplus) {  // the same exponentials of the score 0 as were added
-          const float poly = sfu ? 0.f : (float)(gone >> 16);
-          l -= ((float)(gone & 0xffffu) - poly) * ex2(-m_ref) +
-               poly * ex2_poly4(make_float2(-m_ref, -m_ref)).x;
-        }
         tmem_wait_st();
         tc_fence_before();
         mbar_arrive(&bars.p_full[x]);
