@@ -553,10 +553,30 @@ def forward(Q, K, V, block, row_ptr, col_idx, csr_per_head, mode, stats=None, sc
     return O, lse
 
 
-def _used_on(stream, t):
-    """Keep what a helper allocated on the current stream until `stream` has used it."""
-    if stream is not None:
-        t.record_stream(stream)
+# With `stream` given, a helper's inputs have to be ready on that stream, and the caller orders the
+# result's use after it.
+def _empty(like, shape, stream, dtype=None):
+    """What a helper gives back: memory that `stream`, or the current one, may write at once. A block
+    of the current stream's pool may still be in use by what that stream has queued, so with a
+    stream given the memory comes from that stream's pool; it is kept for the current stream too,
+    where the caller has it."""
+    if stream is None:
+        return like.new_empty(shape, dtype=dtype)
+    with torch.cuda.stream(stream):
+        t = like.new_empty(shape, dtype=dtype)
+    t.record_stream(torch.cuda.current_stream(like.device))
+    return t
+
+
+def _scratch(like, n, stream):
+    """n bytes of workspace of `stream`, or of the current one; None for 0. Freed when the helper
+    returns, it goes to work that the same stream does later."""
+    if n == 0:
+        return None
+    if stream is None:
+        return like.new_empty((n,), dtype=torch.uint8)
+    with torch.cuda.stream(stream):
+        return like.new_empty((n,), dtype=torch.uint8)
 
 
 def rotary(X, pos, axis_dims, base=10000.0, pairing=PAIR_ADJACENT, inverse=False, out=None,
@@ -570,8 +590,7 @@ def rotary(X, pos, axis_dims, base=10000.0, pairing=PAIR_ADJACENT, inverse=False
         return out
     xs = _view(X, "X")
     _four(X, "X")
-    out = X.new_empty(X.shape)
-    _used_on(stream, out)
+    out = _empty(X, X.shape, stream)
     _rotary(X, xs, out, None, pos, axis_dims, base, pairing, inverse, stream)
     return out
 
@@ -584,15 +603,11 @@ def linear(X, W, bias=None, act=ACT_NONE, gate=None, residual=None, heads=0, sta
     xs = _view(X, "X")
     dims = Bt, L, K, N, _ = _linear_shape(X, W, heads)
     if ws is None:
-        need = (_lib or lib()).bsa_linear_workspace_bytes(Bt, L, K, N)
-        if need:
-            ws = torch.empty(need, dtype=torch.uint8, device=X.device)
-            _used_on(stream, ws)
+        ws = _scratch(X, (_lib or lib()).bsa_linear_workspace_bytes(Bt, L, K, N), stream)
     if out is not None:
         bsa_linear(X, W, out, bias, act, gate, residual, ws, status, stream)
         return out
-    out = X.new_empty((Bt, heads, L, N // heads) if heads else (Bt, L, N))
-    _used_on(stream, out)
+    out = _empty(X, (Bt, heads, L, N // heads) if heads else (Bt, L, N), stream)
     ptr, ws_bytes = _workspace_of(ws, X.get_device())
     _linear(X, xs, W, out, None, heads or 1, dims, bias, act, gate, residual, ptr, ws_bytes, status,
             stream)
@@ -609,17 +624,11 @@ def cross_forward(Q, K, V, key_len=None, key_mask=None, scale=0.0, want_lse=Fals
     if not isinstance(K, torch.Tensor) or K.dim() != 4:
         raise ValueError("K must be a [Bt, Hkv, Lk, d] tensor")
     Bt, H, Lq, d = Q.shape
-    O, os_ = (Q.new_empty(Q.shape), None) if out is None else (out, _view(out, "out", Q, Q.shape))
-    lse = Q.new_empty((Bt, H, Lq), dtype=torch.float32) if want_lse else None
+    O, os_ = (_empty(Q, Q.shape, stream), None) if out is None else (out, _view(out, "out", Q, Q.shape))
+    lse = _empty(Q, (Bt, H, Lq), stream, torch.float32) if want_lse else None
     if ws is None:
-        need = (_lib or lib()).bsa_cross_workspace_bytes(Bt, H, K.shape[1], Lq, K.shape[2], d)
-        if need:
-            ws = torch.empty(need, dtype=torch.uint8, device=Q.device)
-            _used_on(stream, ws)
-    if stream is not None:
-        _used_on(stream, O)
-        if want_lse:
-            _used_on(stream, lse)
+        ws = _scratch(Q, (_lib or lib()).bsa_cross_workspace_bytes(Bt, H, K.shape[1], Lq, K.shape[2], d),
+                      stream)
     ptr, ws_bytes = _workspace_of(ws, Q.get_device())
     _cross(Q, qs, K, V, O, os_, key_len, key_mask, scale, lse, ptr, ws_bytes, status, stream)
     return O, lse
