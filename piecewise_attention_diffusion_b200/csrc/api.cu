@@ -63,6 +63,12 @@ bsa_status check_strides(const bsa_strides& s, int elem_bytes) {
   return BSA_OK;
 }
 
+// Rows, columns and tiles of a product are counted in 32 bits. (Sizes > 0.)
+bool linear_sizes_fit(int Bt, int L, int K, int N) {
+  return (int64_t)Bt * L < (int64_t)1 << 30 && K < 1 << 30 && N < 1 << 30 &&
+         (((int64_t)L + 255) / 256 * Bt) * (((int64_t)N + 63) / 64) < INT32_MAX;
+}
+
 bsa_status check_cross(int Bt, int H, int Hkv, int Lq, int Lk, int d) {
   if (Bt <= 0 || H <= 0 || Hkv <= 0 || Lq <= 0 || Lk < 0) return BSA_ERR_INVALID_ARG;
   if (H % Hkv != 0) return BSA_ERR_INVALID_ARG;
@@ -269,7 +275,7 @@ bsa_status bsa_rotary(const void* X, const bsa_strides* xs, void* Y, const bsa_s
 }
 
 size_t bsa_linear_workspace_bytes(int32_t Bt, int32_t L, int32_t K, int32_t N) {
-  if (Bt <= 0 || L <= 0 || K <= 0 || N <= 0) return 0;
+  if (Bt <= 0 || L <= 0 || K <= 0 || N <= 0 || !linear_sizes_fit(Bt, L, K, N)) return 0;
   return bsa::linear_workspace(Bt, L, K, N);
 }
 
@@ -288,11 +294,7 @@ static bsa_status linear_call(uint64_t wait_ns, const void* X, const bsa_strides
     return type == BSA_TYPE_FP32 ? BSA_ERR_UNSUPPORTED : BSA_ERR_INVALID_ARG;
   if ((x_heads > 1 && K / x_heads % 64 != 0) || (y_heads > 1 && N / y_heads % 64 != 0))
     return BSA_ERR_UNSUPPORTED;
-  // rows, columns and tiles are counted in 32 bits
-  if ((int64_t)Bt * L >= (int64_t)1 << 30 || K >= 1 << 30 || N >= 1 << 30)
-    return BSA_ERR_UNSUPPORTED;
-  if ((((int64_t)L + 255) / 256 * Bt) * (((int64_t)N + 63) / 64) >= INT32_MAX)
-    return BSA_ERR_UNSUPPORTED;
+  if (!linear_sizes_fit(Bt, L, K, N)) return BSA_ERR_UNSUPPORTED;
   if (!aligned16(X) || !aligned16(W)) return BSA_ERR_INVALID_ARG;
   for (const void* v : {bias, gate, R, static_cast<const void*>(Y)})
     if ((reinterpret_cast<uintptr_t>(v) & 1u) != 0) return BSA_ERR_INVALID_ARG;
