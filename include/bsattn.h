@@ -340,7 +340,8 @@ typedef enum {
   BSA_ACT_SILU = 3       /* z / (1 + e^-z)                                    */
 } bsa_act;
 
-/* Bytes of device workspace bsa_linear needs; 0 if none, or for sizes that it refuses. */
+/* Bytes of device workspace bsa_linear needs on the current device (how the work is split depends
+ * on its SMs); 0 if none, or for sizes that it refuses. */
 BSA_API size_t bsa_linear_workspace_bytes(int32_t Bt, int32_t L, int32_t K, int32_t N);
 
 /* bsa_linear — matrix product with bias, activation, gate and residual:
@@ -374,7 +375,8 @@ BSA_API bsa_status bsa_linear(const void* X, const bsa_strides* xs, int32_t x_he
                               int32_t L, int32_t K, int32_t N, void* workspace,
                               size_t ws_bytes, int32_t* status, void* stream);
 
-/* Bytes of device workspace bsa_cross_forward needs; 0 if none, or for sizes that it refuses. */
+/* Bytes of device workspace bsa_cross_forward needs on the current device (as for bsa_linear); 0
+ * if none, or for sizes that it refuses. */
 BSA_API size_t bsa_cross_workspace_bytes(int32_t Bt, int32_t H, int32_t Hkv, int32_t Lq,
                                          int32_t Lk, int32_t d);
 

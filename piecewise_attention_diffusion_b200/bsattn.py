@@ -568,6 +568,15 @@ def _empty(like, shape, stream, dtype=None):
     return t
 
 
+def _bytes_on(index, query, *sizes):
+    """What a size query answers for device `index`: the plans behind it count that device's SMs."""
+    f = getattr(_lib or lib(), query)
+    if index == torch._C._cuda_getDevice():
+        return f(*sizes)
+    with torch.cuda.device(index):
+        return f(*sizes)
+
+
 def _scratch(like, n, stream):
     """n bytes of workspace of `stream`, or of the current one; None for 0. Freed when the helper
     returns, it goes to work that the same stream does later."""
@@ -603,7 +612,7 @@ def linear(X, W, bias=None, act=ACT_NONE, gate=None, residual=None, heads=0, sta
     xs = _view(X, "X")
     dims = Bt, L, K, N, _ = _linear_shape(X, W, heads)
     if ws is None:
-        ws = _scratch(X, (_lib or lib()).bsa_linear_workspace_bytes(Bt, L, K, N), stream)
+        ws = _scratch(X, _bytes_on(X.get_device(), "bsa_linear_workspace_bytes", Bt, L, K, N), stream)
     if out is not None:
         bsa_linear(X, W, out, bias, act, gate, residual, ws, status, stream)
         return out
@@ -627,8 +636,8 @@ def cross_forward(Q, K, V, key_len=None, key_mask=None, scale=0.0, want_lse=Fals
     O, os_ = (_empty(Q, Q.shape, stream), None) if out is None else (out, _view(out, "out", Q, Q.shape))
     lse = _empty(Q, (Bt, H, Lq), stream, torch.float32) if want_lse else None
     if ws is None:
-        ws = _scratch(Q, (_lib or lib()).bsa_cross_workspace_bytes(Bt, H, K.shape[1], Lq, K.shape[2], d),
-                      stream)
+        ws = _scratch(Q, _bytes_on(Q.get_device(), "bsa_cross_workspace_bytes", Bt, H, K.shape[1], Lq,
+                                   K.shape[2], d), stream)
     ptr, ws_bytes = _workspace_of(ws, Q.get_device())
     _cross(Q, qs, K, V, O, os_, key_len, key_mask, scale, lse, ptr, ws_bytes, status, stream)
     return O, lse

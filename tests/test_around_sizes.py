@@ -49,3 +49,59 @@ def test_any_sizes_are_answered():
         if b.bsa_cross_workspace_bytes(*sizes):
             assert _cross(**dict(zip(("Bt", "H", "Hkv", "Lq", "Lk", "d"), sizes)), ws=None) in (
                 b.ERR_WORKSPACE, b.ERR_UNSUPPORTED, b.ERR_INVALID_ARG)
+
+
+class _Devices:
+    """A current device and a library whose plans count its SMs, without a GPU."""
+    sms = (148, 74)
+
+    def __init__(self):
+        self.now = 0
+
+    def device(self, index):
+        outer = self
+
+        class Context:
+            def __enter__(self):
+                self.before, outer.now = outer.now, index
+
+            def __exit__(self, *_):
+                outer.now = self.before
+        return Context()
+
+    def bsa_linear_workspace_bytes(self, *sizes):
+        return self.sms[self.now] * sum(sizes)
+
+    bsa_cross_workspace_bytes = bsa_linear_workspace_bytes
+
+
+@pytest.mark.parametrize("query", ["bsa_linear_workspace_bytes", "bsa_cross_workspace_bytes"])
+def test_helpers_ask_for_the_tensors_device(monkeypatch, query):
+    dev = _Devices()
+    monkeypatch.setattr(b, "_lib", dev)
+    monkeypatch.setattr(b.torch._C, "_cuda_getDevice", lambda: dev.now, raising=False)
+    monkeypatch.setattr(b.torch.cuda, "device", dev.device)
+    asked = []
+    monkeypatch.setattr(b, "_scratch", lambda like, n, stream: asked.append(n))
+    # a helper is run up to its launch with stand-ins of tensors on device 1
+    monkeypatch.setattr(b, "_view", lambda *a, **k: None)
+    monkeypatch.setattr(b, "_empty", lambda *a, **k: None)
+    for name in ("_linear", "_cross"):
+        monkeypatch.setattr(b, name, lambda *a, **k: None)
+    monkeypatch.setattr(b, "_workspace_of", lambda ws, index: (None, 0))
+    meta = lambda *shape: _OnDevice1(b.torch.empty(*shape, device="meta"))
+    if query == "bsa_linear_workspace_bytes":
+        b.linear(meta(1, 4, 64), b.torch.empty(32, 64, device="meta"))
+        want = 74 * (1 + 4 + 64 + 32)
+    else:
+        b.cross_forward(meta(1, 2, 3, 64), b.torch.empty(1, 2, 9, 64, device="meta"), None)
+        want = 74 * (1 + 2 + 2 + 3 + 9 + 64)
+    assert asked == [want] and dev.now == 0
+
+
+class _OnDevice1:
+    def __init__(self, t):
+        self.shape, self.dim = t.shape, t.dim
+
+    def get_device(self):
+        return 1
