@@ -19,6 +19,7 @@
 #include <algorithm>
 
 #include "common.cuh"
+#include "forward_tiles.cuh"
 #include "internal.h"
 #include "types.cuh"
 
@@ -207,15 +208,16 @@ cudaError_t run(Params& p, cudaStream_t st) {
   const int64_t ctas = (p.n * p.groups + kThreads - 1) / kThreads;
   // all heads in one thread share its sines; fewer per thread where that leaves the card
   // short of CTAs
-  const int64_t want = 148 * 8;
+  const int sms = fwdtiles::sm_count();
+  const int64_t want = sms * 8;
   int split = (int)std::min<int64_t>(ceil_div(p.H, kUnroll), (want + ctas - 1) / ctas);
   p.heads_per_cta = ceil_div(ceil_div(p.H, split), kUnroll) * kUnroll;
   const unsigned heads = (unsigned)ceil_div(p.H, p.heads_per_cta);
   // A thread with one pair of few heads ends before its CTA's tables have paid. bf16, halves paired,
   // odd sections of 128, 4 entries: 3 heads x 30323 tokens 89 us, 172 with CTAs for all; 16 x 12000
   // 99, 105.
-  if (W == 1 && p.heads_per_cta <= 4 * kUnroll && ctas > 16 * 148)
-    k_rotary<T, W, kAdjacent, W == 1><<<dim3(16 * 148, heads), kThreads, 0, st>>>(p);
+  if (W == 1 && p.heads_per_cta <= 4 * kUnroll && ctas > 16 * sms)
+    k_rotary<T, W, kAdjacent, W == 1><<<dim3(16 * sms, heads), kThreads, 0, st>>>(p);
   else
     k_rotary<T, W, kAdjacent, false><<<dim3((unsigned)ctas, heads), kThreads, 0, st>>>(p);
   return cudaGetLastError();
