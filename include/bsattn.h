@@ -321,9 +321,11 @@ typedef enum {
  *            X with the same strides (in place); any other overlap is undefined;
  *   d        a multiple of 8, at most 256;
  *   pos      device fp32 [L, n_axes], or [Bt, L, n_axes] with pos_per_batch nonzero; a
- *            text token at position 0 of every axis is left as it is. Angles are reduced
- *            in 64 bits: positions of any size a float holds exactly are turned exactly.
- *            A position that is not finite makes its token's rotated components NaN;
+ *            text token at position 0 of every axis is left as it is. Angles are formed
+ *            and reduced in 64 bits: besides the rounding of a sine to fp32, an angle is off
+ *            by less than |pos| 2^-50 radians (up to positions of 2^26 less than that
+ *            rounding; at 2^40 up to 2^-10). A position that is not finite makes its
+ *            token's rotated components NaN;
  *   axis_dim host int32[n_axes], each even and >= 2, their sum at most d; 1 <= n_axes <= 4;
  *   base     > 1, finite.
  * Arithmetic is fp32, rounded once to `type`. */
