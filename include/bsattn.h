@@ -412,8 +412,9 @@ BSA_API bsa_status bsa_cross_forward(const void* Q, const bsa_strides* qs, const
                                      const bsa_strides* os, float* lse, void* workspace,
                                      size_t ws_bytes, int32_t* status, void* stream);
 
-/* bsa_selftest_linear_timeout, bsa_selftest_cross_timeout — the abort paths of bsa_linear's and
- * bsa_cross_forward's kernels, run without a fault, as bsa_selftest_forward_timeout runs that of
+/* bsa_selftest_linear_timeout, bsa_selftest_cross_timeout, bsa_selftest_cross_mask_timeout — the
+ * abort paths of bsa_linear's and bsa_cross_forward's kernels (the last one's that of the kernel
+ * for a key_mask, uint8 [Lk]), run without a fault, as bsa_selftest_forward_timeout runs that of
  * bsa_forward: the same launch sequence on contiguous tensors (X [L, K], W [N, K], Y [L, N], no
  * bias, gate or residual; Q, O [H, Lq, d], K, V [H, Lk, d]) with every bounded wait limited to
  * wait_ns. With a limit far below the time of a copy a wait runs out while copies and products
@@ -430,6 +431,12 @@ BSA_API bsa_status bsa_selftest_cross_timeout(const void* Q, const void* K, cons
                                               int32_t d, const int32_t* key_len, void* workspace,
                                               size_t ws_bytes, int64_t wait_ns, int32_t* status,
                                               void* stream);
+BSA_API bsa_status bsa_selftest_cross_mask_timeout(const void* Q, const void* K, const void* V,
+                                                   void* O, int32_t type, int32_t H, int32_t Lq,
+                                                   int32_t Lk, int32_t d, const int32_t* key_len,
+                                                   const uint8_t* key_mask, void* workspace,
+                                                   size_t ws_bytes, int64_t wait_ns,
+                                                   int32_t* status, void* stream);
 
 #ifdef __cplusplus
 }

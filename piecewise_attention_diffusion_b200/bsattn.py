@@ -37,7 +37,7 @@ EXPORTS = ("bsa_version", "bsa_status_string", "bsa_mask_blocks", "bsa_workspace
            "bsa_forward_noalloc", "bsa_selftest_wait_timeout", "bsa_selftest_forward_timeout",
            "bsa_rotary", "bsa_linear_workspace_bytes", "bsa_linear",
            "bsa_cross_workspace_bytes", "bsa_cross_forward", "bsa_selftest_linear_timeout",
-           "bsa_selftest_cross_timeout")
+           "bsa_selftest_cross_timeout", "bsa_selftest_cross_mask_timeout")
 
 
 class BsaError(RuntimeError):
@@ -90,6 +90,8 @@ _SIGS = {
                                            _vp, _vp]),
     "bsa_selftest_cross_timeout": (_i32, [_vp, _vp, _vp, _vp, _i32, _i32, _i32, _i32, _i32, _vp,
                                           _vp, _sz, _i64, _vp, _vp]),
+    "bsa_selftest_cross_mask_timeout": (_i32, [_vp, _vp, _vp, _vp, _i32, _i32, _i32, _i32, _i32,
+                                               _vp, _vp, _vp, _sz, _i64, _vp, _vp]),
 }
 
 
@@ -483,13 +485,26 @@ def bsa_selftest_linear_timeout(X, W, Y, workspace, wait_ns, status, stream=None
 def bsa_selftest_cross_timeout(Q, K, V, O, workspace, wait_ns, status, key_len=None, stream=None):
     """bsa_cross_forward of Q [H, Lq, d], K, V [H, Lk, d] with every bounded wait limited to
     wait_ns: the kernel's abort and drain path, reported as BSA_ERR_TIMEOUT in `status`."""
+    _cross_timeout("bsa_selftest_cross_timeout", Q, K, V, O, (), workspace, wait_ns, status, key_len,
+                   stream)
+
+
+def bsa_selftest_cross_mask_timeout(Q, K, V, O, key_mask, workspace, wait_ns, status, key_len=None,
+                                    stream=None):
+    """The same of the kernel for a key_mask, uint8 [Lk]."""
+    mask = _plain(key_mask, torch.uint8, "key_mask", (K.shape[1],), Q.get_device())
+    _cross_timeout("bsa_selftest_cross_mask_timeout", Q, K, V, O, (mask,), workspace, wait_ns, status,
+                   key_len, stream)
+
+
+def _cross_timeout(fn, Q, K, V, O, mask, workspace, wait_ns, status, key_len, stream):
     dev, dt = Q.get_device(), Q.dtype
     (H, Lq, d), Lk = Q.shape, K.shape[1]
     ws, ws_bytes = _workspace_of(workspace, dev)
-    _call("bsa_selftest_cross_timeout", dev, stream, _plain(Q, dt, "Q", (H, Lq, d), dev),
+    _call(fn, dev, stream, _plain(Q, dt, "Q", (H, Lq, d), dev),
           _plain(K, dt, "K", (H, Lk, d), dev), _plain(V, dt, "V", (H, Lk, d), dev),
           _plain(O, dt, "O", (H, Lq, d), dev), TYPES[dt], H, Lq, Lk, d,
-          _plain(key_len, torch.int32, "key_len", (1,), dev), ws, ws_bytes, int(wait_ns),
+          _plain(key_len, torch.int32, "key_len", (1,), dev), *mask, ws, ws_bytes, int(wait_ns),
           _plain(status, torch.int32, "status", (1,), dev))
 
 

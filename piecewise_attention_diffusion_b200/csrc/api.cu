@@ -395,9 +395,18 @@ bsa_status bsa_selftest_cross_timeout(const void* Q, const void* K, const void* 
                                       int32_t type, int32_t H, int32_t Lq, int32_t Lk, int32_t d,
                                       const int32_t* key_len, void* workspace, size_t ws_bytes,
                                       int64_t wait_ns, int32_t* status, void* stream) {
+  return bsa_selftest_cross_mask_timeout(Q, K, V, O, type, H, Lq, Lk, d, key_len, nullptr, workspace,
+                                         ws_bytes, wait_ns, status, stream);
+}
+
+bsa_status bsa_selftest_cross_mask_timeout(const void* Q, const void* K, const void* V, void* O,
+                                           int32_t type, int32_t H, int32_t Lq, int32_t Lk, int32_t d,
+                                           const int32_t* key_len, const uint8_t* key_mask,
+                                           void* workspace, size_t ws_bytes, int64_t wait_ns,
+                                           int32_t* status, void* stream) {
   if (status == nullptr || wait_ns < 1 || wait_ns > 10000000000ll) return BSA_ERR_INVALID_ARG;
   return cross_call(static_cast<uint64_t>(wait_ns), Q, nullptr, K, nullptr, V, nullptr, type, 1, H, H,
-                    Lq, Lk, d, key_len, nullptr, 0.f, O, nullptr, nullptr, workspace, ws_bytes,
+                    Lq, Lk, d, key_len, key_mask, 0.f, O, nullptr, nullptr, workspace, ws_bytes,
                     status, stream);
 }
 
