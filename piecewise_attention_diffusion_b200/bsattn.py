@@ -454,6 +454,8 @@ def _cross(Q, qs, K, V, O, os_, key_len, key_mask, scale, lse, ws, ws_bytes, sta
         raise ValueError(f"K has shape {tuple(K.shape)}, Q {tuple(Q.shape)}")
     Hkv, Lk = K.shape[1], K.shape[2]
     index = Q.get_device()
+    if isinstance(key_mask, torch.Tensor) and key_mask.dtype == torch.bool:
+        key_mask = key_mask.view(torch.uint8)  # the same bytes
     _call("bsa_cross_forward", index, stream, Q.data_ptr(), qs, K.data_ptr(), ks, V.data_ptr(), vs,
           TYPES[Q.dtype], Bt, H, Hkv, Lq, Lk, d,
           _plain(key_len, torch.int32, "key_len", (Bt,), index),
@@ -641,8 +643,8 @@ def linear(X, W, bias=None, act=ACT_NONE, gate=None, residual=None, heads=0, sta
 def cross_forward(Q, K, V, key_len=None, key_mask=None, scale=0.0, want_lse=False, status=None,
                   ws=None, out=None, stream=None):
     """Attention of Q [Bt, H, Lq, d] over K, V [Bt, Hkv, Lk, d] (any strides; H a multiple of
-    Hkv): the first key_len[b] (int32 [Bt]) keys of each entry, those whose key_mask (uint8
-    [Bt, Lk]) is not 0, or all. Returns (O contiguous or `out`, lse fp32 [Bt, H, Lq] or None)."""
+    Hkv): the first key_len[b] (int32 [Bt]) keys of each entry, those whose key_mask (uint8 or
+    bool [Bt, Lk]) is not 0, or all. Returns (O contiguous or `out`, lse fp32 [Bt, H, Lq] or None)."""
     qs = _view(Q, "Q")
     _four(Q, "Q")
     if not isinstance(K, torch.Tensor) or K.dim() != 4:

@@ -88,3 +88,17 @@ def test_queries_that_are_not_finite_over_no_real_key(d):
     z = torch.zeros((), dtype=k.dtype, device=DEV)
     _check(o[:, :, keep], lse[:, :, keep], q[:, :, keep], torch.where(torch.isfinite(k), k, z), v,
            key_mask=mask)
+
+
+@pytest.mark.parametrize("Lq", [2, 150])
+def test_a_mask_of_truth_values(Lq):
+    q, k, v = _randn(2, 2, Lq, 64), _randn(2, 2, 500, 64, seed=1), _randn(2, 2, 500, 64, seed=2)
+    mask = torch.arange(1000, device=DEV).view(2, 500) % 3 != 0
+    o, lse = b.cross_forward(q, k, v, key_mask=mask, want_lse=True)
+    _check(o, lse, q, k, v, key_mask=mask)
+    want, _ = b.cross_forward(q, k, v, key_mask=mask.to(torch.uint8))
+    assert torch.equal(o, want)
+    with pytest.raises(ValueError, match="key_mask"):
+        b.cross_forward(q, k, v, key_mask=mask.int())
+    with pytest.raises(ValueError, match="key_mask"):
+        b.cross_forward(q, k, v, key_mask=mask.t().contiguous().t())
