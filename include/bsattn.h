@@ -399,7 +399,8 @@ BSA_API size_t bsa_cross_workspace_bytes(int32_t Bt, int32_t H, int32_t Hkv, int
  *            never matters;
  *   scale    0 selects 1/sqrt(d);
  *   lse      nullable fp32 [Bt, H, Lq]: the natural logarithm of the denominator.
- * A row without a real key outputs zeros and lse = -inf.
+ * A row without a real key outputs zeros and lse = -inf, as does one whose real keys all have the
+ * score -inf. O must not overlap Q, K or V.
  *   workspace  device, >= bsa_cross_workspace_bytes(...) bytes, contents scratch: with few
  *            query rows the keys are split over the GPU and their parts joined (always in one
  *            order: the same bits on every run);

@@ -57,6 +57,7 @@ constexpr int kBK = 128;  // keys per tile
 constexpr int kStreams = 2;
 constexpr int kThreads = 384;
 constexpr int kProducerWarp = 8, kMmaWarp = 9, kClearKWarp = 10, kClearVWarp = 11;
+static_assert(kClearKWarp == kMmaWarp + 1 && kClearVWarp == kThreads / 32 - 1, "the last two warps clear");
 // register split as in the block attention: 128 x 88 + 256 x 208 = 384 x 168
 constexpr int kRegsControl = 88, kRegsSoftmax = 208;
 static_assert(128 * kRegsControl + 256 * kRegsSoftmax <= kThreads * 168, "register split");
@@ -181,7 +182,11 @@ __device__ __forceinline__ float2 ex2_poly4(float2 x) {
 constexpr int kPolyOf8 = 2;
 
 // P of one row: 2^(s * scale_log2 - m_ref), to TMEM in pairs of T at p_addr, arriving at `half`
-// when the first 64 keys are there; returns the fp32 sum.
+// when the first 64 keys are there; returns the fp32 sum, of the weights before they are rounded.
+// The rounding to T (2^-8 of a weight at most in bf16, 2^-11 in fp16, to nearest) is what the tensor
+// core asks for, whose two operands have V's type. Against 64 bits an output is then off by 2.3e-3
+// in bf16 (2.5e-4 in fp16), where 32-bit weights would give 1.7e-3 (2.1e-4), most of which is the
+// output's own rounding; weights in two 16-bit parts would double the second product.
 template <typename T, int kPoly>
 __device__ __forceinline__ float row_exp(const uint32_t (&r)[kBK], float scale_log2, float m_ref,
                                          uint32_t p_addr, uint64_t* half) {
