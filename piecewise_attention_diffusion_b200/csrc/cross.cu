@@ -22,8 +22,8 @@
 //   warp 10 clears those rows of K where there is a key mask, so that their scores are 0, and
 //           leaves the softmax a term per key, 0 or -inf, which is added to the scores: two keys
 //           an instruction, where a select per score took three instructions a key (2 x 16 heads x
-//           4101 queries x 4352 keys, a fifth masked: 287 us whatever the scores; 325 with the
-//           select). To let the zeros through and take their exponentials off the sum again took
+//           4101 queries x 4352 keys, a fifth masked: 287 us after idle time, 321 call after call,
+//           whatever the scores; 325 after idle time with the select). To let the zeros through and take their exponentials off the sum again took
 //           278 us where the scores allowed it, but what rounding left of them grew with the
 //           number of tiles: 2.7e-4 of a sum after 256. Rows are cleared four at a time, a bit
 //           per row; row by row took 4% more.
@@ -33,9 +33,13 @@
 // as one head of more rows where their strides allow it (always for one row; 8 x 40 heads of one
 // query over 8 key heads x 8192 keys x 128: 54 us, a tile for each query head 285).
 // Measured, bf16, K and V read once, out of L2: 40 heads x 16384 queries x 512 keys x 128 in
-// 163 us, 1054 TFLOP/s, the tensor pipe at 53% of its cycles. What bounds it is the chain of one
-// stream's step (scores, maximum, exponentials, P, products: about 2950 cycles for the two
-// streams' 2048 cycles of products), not the exponentials' pipe (41%) nor memory.
+// 162 us after idle time, 1061 TFLOP/s, and in 191 us call after call, where the power limit holds
+// the SMs at 1.54 GHz of 1.965; the tensor pipe is busy 53% of the cycles. What bounds it is the chain
+// of one stream's step (scores, maximum, exponentials, P, products: about 2930 cycles for the two
+// streams' 2048 cycles of products) and the turn from one item to the next: 2100 of the 13900
+// cycles of an item of four steps, in which the first scores wait until the last P is taken and the
+// softmax warps write O. (Cycles per item at 512, 1024 and 2048 keys: 13900, 26000, 49000.) It is
+// not the exponentials' pipe (41%) nor memory.
 // Every mbarrier wait is bounded; on a timeout the CTA drains, frees TMEM and reports
 // BSA_ERR_TIMEOUT.
 #include <algorithm>

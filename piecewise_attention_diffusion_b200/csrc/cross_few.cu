@@ -14,8 +14,8 @@
 // gets CTAs in proportion to the real keys of its batch entry (cross_share.cuh; every CTA finds
 // the same shares from the key counts), so that short entries leave no SM idle while a long one
 // is read: 8 x 16 heads with 50 to 8192 keys of 8192 x 128 take 56 us, with as many CTAs for each head 99.
-// 2 x 16 heads x 32768 keys x 64: 51 us for 268 MB, 5.2 TB/s (the tensor-core kernel's split
-// tiles: 92 us); with a fifth of the keys masked 53 us (113).
+// 2 x 16 heads x 32768 keys x 64: 54 us with the join for 268 MB, 5.0 TB/s (the tensor-core kernel's
+// split tiles: 92 us); one entry with half of them, 201 MB: 43.6 us; a fifth masked: 53 us (113).
 #include "common.cuh"
 #include "cross_share.cuh"
 #include "internal.h"

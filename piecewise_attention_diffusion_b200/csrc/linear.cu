@@ -19,9 +19,11 @@
 //              gate and residual in fp32, one rounding, back into the buffer, and a TMA store.
 //              (Where strides rule TMA out: coalesced 2-byte accesses, 16 rows at a time.) Two
 //              TMEM accumulators, so the epilogue of one tile runs under the products of the next.
-// Measured out of L2, bf16: 16384 x 5120 x 5120 with bias, gate and residual 556-690 us (by the
-// power limit; 1.25-1.55 PFLOP/s), the tensor pipe at 93%; 9216 x 1024 x 4096 with GELU 66 us,
-// bound by the epilogue, whose warps wait on one latency after the other; 23240 x 400 x 2560 with
+// Measured out of L2, bf16: 16384 x 5120 x 5120 with bias, gate and residual 585 us after idle time
+// and 690 call after call, where the power limit holds the SMs at 1.24 GHz of 1.965 (1.24-1.47
+// PFLOP/s), the tensor pipe at 93%; 9216 x 1024 x 4096 with GELU (fp16) 66 and 78 us (1.4 GHz), the
+// tensor pipe at 69%: a tile takes 11500 cycles, of which 8200 are products, as the epilogue's warps
+// wait on one latency after the other; 23240 x 400 x 2560 with
 // GELU (erf), gate and residual 109 us (177 with CUDA's erfcf); 2928 x 168 x 19968 with a residual
 // 83 us where 16-byte loads of it by the lanes that own its rows took 126. Chunks are 32 columns
 // because boxes of 64 (128-byte rows), stored once per tile, delay the operands' loads: 2.3% more

@@ -9,7 +9,7 @@
 // loaded before the first is turned, the first of them before the sines are formed.
 // Inputs out of L2: 40 heads x 16384 tokens x 128 bf16 components in 55.4 us, 6.07 TB/s of
 // reads and writes (56.5 with the sines first); 2 x 12 heads x 4099 tokens x 120 fp32
-// components in 18.3 us, 5.2 TB/s (20.0).
+// components in 18.3 to 19.3 us, 4.9 to 5.2 TB/s (20.0).
 //
 // The angle is formed in 64 bits as a number of turns, pos * base^(-2 i / axis_dim) / 2 pi,
 // whose whole part is dropped before rounding to fp32: in 32 bits the angle of position
