@@ -585,6 +585,13 @@ def _empty(like, shape, stream, dtype=None):
     return t
 
 
+def _given(out, stream):
+    """A caller's output, kept until `stream` has written it even if the caller lets go of it."""
+    if stream is not None:
+        out.record_stream(stream)
+    return out
+
+
 def _bytes_on(index, query, *sizes):
     """What a size query answers for device `index`: the plans behind it count that device's SMs."""
     f = getattr(_lib or lib(), query)
@@ -613,7 +620,7 @@ def rotary(X, pos, axis_dims, base=10000.0, pairing=PAIR_ADJACENT, inverse=False
     itself). inverse turns back, which also takes gradients through the rotation."""
     if out is not None:
         bsa_rotary(X, out, pos, axis_dims, base, pairing, inverse, stream)
-        return out
+        return _given(out, stream)
     xs = _view(X, "X")
     _four(X, "X")
     out = _empty(X, X.shape, stream)
@@ -632,7 +639,7 @@ def linear(X, W, bias=None, act=ACT_NONE, gate=None, residual=None, heads=0, sta
         ws = _scratch(X, _bytes_on(X.get_device(), "bsa_linear_workspace_bytes", Bt, L, K, N), stream)
     if out is not None:
         bsa_linear(X, W, out, bias, act, gate, residual, ws, status, stream)
-        return out
+        return _given(out, stream)
     out = _empty(X, (Bt, heads, L, N // heads) if heads else (Bt, L, N), stream)
     ptr, ws_bytes = _workspace_of(ws, X.get_device())
     _linear(X, xs, W, out, None, heads or 1, dims, bias, act, gate, residual, ptr, ws_bytes, status,
@@ -657,7 +664,7 @@ def cross_forward(Q, K, V, key_len=None, key_mask=None, scale=0.0, want_lse=Fals
                                    K.shape[2], d), stream)
     ptr, ws_bytes = _workspace_of(ws, Q.get_device())
     _cross(Q, qs, K, V, O, os_, key_len, key_mask, scale, lse, ptr, ws_bytes, status, stream)
-    return O, lse
+    return (O if out is None else _given(O, stream)), lse
 
 
 def default_scale(d: int) -> float:

@@ -1,6 +1,7 @@
 """The helpers of the calls around the block attention with a stream given: what they allocate is not
 memory that the current stream, or the given one, may still be using."""
 import gc
+import threading
 
 import pytest
 import torch
@@ -108,3 +109,52 @@ def test_a_stream_of_another_device_is_refused():
     x = _randn(1, 2, 8, 64)
     with pytest.raises(ValueError, match="stream"):
         b.rotary(x, torch.zeros(8, 1, device=DEV), (64,), out=torch.empty_like(x), stream=Other())
+
+
+def test_calls_of_several_host_threads():
+    """Threads that call at once, each on a stream of its own."""
+    calls = [c for n, c, _ in _calls() if n != "linear out"]
+    want = [[t.clone() for t in c(None)] for c in calls]
+    torch.cuda.synchronize()
+    wrong = []
+
+    def work():
+        s = torch.cuda.Stream()
+        with torch.cuda.stream(s):
+            for _ in range(20):
+                for i, c in enumerate(calls):
+                    got = c(None)
+                    s.synchronize()
+                    if not all(torch.equal(g, w) for g, w in zip(got, want[i])):
+                        wrong.append(i)
+
+    threads = [threading.Thread(target=work) for _ in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong
+
+
+def test_an_output_of_the_caller_that_is_let_go():
+    """Memory of a caller's output is not given out while the given stream has yet to write it."""
+    x, w = _randn(1, 4, 8192), _randn(1, 256, 8192, seed=1, scale=8192 ** -0.5)[0]
+    q, k = _randn(1, 2, 200, 64), _randn(1, 2, 77, 64, seed=1)
+    pos = torch.zeros(200, 1, device=DEV)
+    s = torch.cuda.Stream()
+    for call, shape in ((lambda o: b.linear(x, w, out=o, stream=s), (1, 4, 256)),
+                        (lambda o: b.cross_forward(q, k, k, out=o, stream=s), q.shape),
+                        (lambda o: b.rotary(q, pos, (64,), out=o, stream=s), q.shape)):
+        out = torch.empty(shape, dtype=q.dtype, device=DEV)
+        torch.cuda.synchronize()
+        with torch.cuda.stream(s):
+            torch.cuda._sleep(20_000_000)
+        call(out)
+        done = torch.cuda.Event()
+        done.record(s)
+        ptr = out.data_ptr()
+        del out
+        fresh = [torch.zeros(shape, dtype=q.dtype, device=DEV) for _ in range(4)]
+        assert done.query() or all(t.data_ptr() != ptr for t in fresh)
+        torch.cuda.synchronize()
+        assert not any(t.any() for t in fresh)
