@@ -23,10 +23,10 @@
 //           leaves the softmax a term per key, 0 or -inf, which is added to the scores: two keys
 //           an instruction, where a select per score took three instructions a key (2 x 16 heads x
 //           4101 queries x 4352 keys, a fifth masked: 287 us after idle time, 321 call after call,
-//           whatever the scores; 325 after idle time with the select). To let the zeros through and take their exponentials off the sum again took
-//           278 us where the scores allowed it, but what rounding left of them grew with the
-//           number of tiles: 2.7e-4 of a sum after 256. Rows are cleared four at a time, a bit
-//           per row; row by row took 4% more.
+//           whatever the scores; 325 after idle time with the select). To let the zeros through
+//           and take their exponentials off the sum again took 278 us where the scores allowed
+//           it, but what rounding left of them grew with the number of tiles: 2.7e-4 of a sum
+//           after 256. Rows are cleared four at a time, a bit per row; row by row took 4% more.
 // TMEM: S0 [0,128), S1 [128,256), O0 [256, 256 + D), O1 [256 + D, 256 + 2 D); P overlays S.
 // Few rows: the keys are split into runs that separate items take; each leaves its O, m and l
 // in the workspace, and k_join adds them in order. Query heads that share a key head are taken
